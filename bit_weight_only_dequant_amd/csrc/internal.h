@@ -89,6 +89,7 @@ struct Call {
 int validate_call(const Call& c, Plan* plan);
 int launch_call(const Call& c, const Plan& p, float* ws, void* stream);
 int call_pointers_ok(const Call& c);
+int check_device_pointers(const void* const* ptrs, int n);   // the same test of n pointers (NULL entries skipped)
 int current_device(int* dev);          // QG_OK when a HIP device is current
 int hip_status(int hip_error);         // QG_OK, or QG_E_DEVICE (and records the error)
 int env_int(const char* name, int dflt);   // integer environment setting (tuning, tests)

@@ -1819,7 +1819,7 @@ static bool pointer_check_on() {
   return v && v[0] == '1' && v[1] == 0;
 }
 
-static int check_device_pointers(const void* const* ptrs, int n) {
+int check_device_pointers(const void* const* ptrs, int n) {
   if (!pointer_check_on()) return QG_OK;
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) {

@@ -301,6 +301,97 @@ int qg_dequant(const uint32_t* packed, const uint16_t* scales, const uint16_t* z
 int qg_plan(int M, int N, int K, int group, int fmt, int out[5]);
 
 /*
+ * Microscaled 4-bit floating point (MXFP4, OCP Microscaling Formats v1.0).
+ *
+ * An MXFP4 matrix [R, K] is two byte arrays, both row-major and contiguous:
+ *   codes  uint8 [R, K/2]   E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 for the
+ *                           codes 0..7, the same negated for 8..15); element
+ *                           2i of a row in the low nibble of its byte i.
+ *   scales uint8 [R, K/32]  E8M0: the byte s is the factor 2^(s - 127) of 32
+ *                           consecutive elements; 255 makes the block NaN.
+ * The products read this form as it is: there is no packing step.
+ * The formats of the framework's own weight codes (qg_format_t) are integers
+ * with fp16 scales; these are the floating-point sibling, for weights and,
+ * unlike those, for activations too.
+ *
+ * Conventions: those at the head of this file, with these differences.
+ * K % 32 == 0.  Codes, x, y and residual are 16-byte aligned; scales have no
+ * alignment; rows, offsets and row_scale are 4-byte aligned.  Leading
+ * dimensions count elements; ldx % 8 == 0 (ldy of qmx_dequantize too).
+ * No entry point uses a workspace: calls may overlap on any streams, and
+ * every one of them may be captured into a HIP graph.
+ */
+typedef enum {
+  QG_MX_F16 = 0,   /* IEEE binary16 */
+  QG_MX_BF16 = 1,  /* bfloat16      */
+  QG_MX_F32 = 2,   /* IEEE binary32 */
+  QG_MX_FP4 = 3    /* MXFP4: codes and scales as above */
+} qg_mx_type_t;
+
+/*
+ * qmx_quantize: x [M, K] -> codes and scales.
+ * Per block of 32, with A its largest magnitude: the scale byte is
+ * max(0, floor(log2 A) - 2 + 127), 0 for A == 0; an element is v / scale
+ * rounded to the nearest E2M1 value, ties to the even code, at most 6 in
+ * magnitude, its sign kept.  A block that holds an infinity or a NaN gets the
+ * scale byte 255 and codes 0, so it reads back as NaN.
+ *   x      [device, in]  x_type QG_MX_F16, QG_MX_BF16 or QG_MX_F32, leading dimension ldx >= K.
+ *   codes, scales [device, out].
+ * Errors: QG_E_ARG, QG_E_ALIGN, QG_E_DEVICE, QG_E_NOT_DEVICE.
+ */
+int qmx_quantize(const void* x, int ldx, int x_type, int M, int K, uint8_t* codes, uint8_t* scales,
+                 void* stream);
+
+/*
+ * qmx_dequantize: codes and scales -> y [M, K] of y_type QG_MX_F16,
+ * QG_MX_BF16 or QG_MX_F32, each value rounded once (to nearest even; exact
+ * for bf16 and fp32 but for values of 2^128 and more, which are infinite).
+ * Errors as qmx_quantize.
+ */
+int qmx_dequantize(const uint8_t* codes, const uint8_t* scales, int M, int K, void* y, int ldy, int y_type,
+                   void* stream);
+
+/*
+ * qmx_gemm: y[M, N] = x[M, K] . W[N, K]^T (+ residual), W in MXFP4; fp32
+ * accumulation and one rounding to y_type at the end.  No element of x or W
+ * is rounded on the way: 16-bit x meets the exact weight values.
+ *   x        [device, in] x_type QG_MX_F16 or QG_MX_BF16 with leading dimension ldx >= K, or
+ *            QG_MX_FP4: codes (then ldx == K) with x_scales [M, K/32].
+ *   x_scales NULL unless x_type is QG_MX_FP4.
+ *   w, w_scales [device, in] MXFP4 [N, K].
+ *   residual [device, in] y_type [M, N] with leading dimension ldr >= N, or NULL.  It may be y
+ *            itself when ldr == ldy.
+ *   y        [device, out] y_type QG_MX_F16, QG_MX_BF16 or QG_MX_F32, leading dimension ldy >= N.
+ * M == 0 or N == 0 is a no-op; K == 0 writes zeros (plus the residual).
+ * Sums are added in a fixed order: equal inputs give equal bits.
+ * Errors: QG_E_ARG, QG_E_ALIGN, QG_E_UNSUPPORTED (more than 2^31 - 1 tiles), QG_E_DEVICE, QG_E_NOT_DEVICE.
+ */
+int qmx_gemm(const void* x, int ldx, int x_type, const uint8_t* x_scales, const uint8_t* w,
+             const uint8_t* w_scales, const void* residual, int ldr, int M, int N, int K, void* y, int ldy,
+             int y_type, void* stream);
+
+/*
+ * qmx_gemm_grouped: T rows in E groups of any sizes, group e multiplied with
+ * its own matrix W[e] -- the experts' products of a mixture of experts whose
+ * rows are sorted by expert:
+ *   y[t, :] = row_scale[t] * (x[rows[t], :] . W[e]^T)   for offsets[e] <= t < offsets[e + 1].
+ *   x, x_scales as qmx_gemm, with x_rows rows.
+ *   rows      [device, in] int32 [T]: the row of x that slot t takes; a value outside [0, x_rows)
+ *             makes the slot's output row zero.  NULL: slot t takes row t (then x_rows >= T).
+ *   w, w_scales [device, in] MXFP4 [E, N, K].
+ *   offsets   [device, in] int32 [E + 1], not decreasing, within [0, T].  They are read on the
+ *             device: nothing waits for them on the host.  Whatever they hold, no access leaves
+ *             the arrays; where they decrease or leave [0, T], what y's rows then hold is unspecified.
+ *   row_scale [device, in] fp32 [T], multiplied in fp32 before the rounding, or NULL.
+ *   y         [device, out] [T, N].  Rows outside [offsets[0], offsets[E]) are left as they were.
+ * Errors as qmx_gemm (QG_E_UNSUPPORTED for E > 65535 too).
+ */
+int qmx_gemm_grouped(const void* x, int ldx, int x_type, const uint8_t* x_scales, int x_rows,
+                     const int32_t* rows, const uint8_t* w, const uint8_t* w_scales, const int32_t* offsets,
+                     int E, int T, const float* row_scale, int N, int K, void* y, int ldy, int y_type,
+                     void* stream);
+
+/*
  * Measurement helpers: the ceilings a qGEMM kernel is read against, taken on
  * the device it runs on (the hot-op microbenchmarks of the TinyLoop README,
  * "Validation", and the phase timings of its "Quick CLI Tour", "Benchmark").

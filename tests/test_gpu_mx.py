@@ -1,0 +1,423 @@
+"""The MXFP4 operators on the GPU against the oracle in 64 bits.
+
+Tolerances.  Quantising and reading back are exact, as are products whose
+terms and partial sums are integers times one power of two below 2^24 (fp32
+holds every partial sum, in any order).  Elsewhere |y - ref| is at most half a
+step of the output type (relative eps / 2, or half its smallest subnormal) plus
+the fp32 sums' own error: at most K + 2 additions (and the factor of row_scale),
+each off by at most a whole unit (2^-23, matrix cores need not round to
+nearest) of a partial sum that the sum of the terms' magnitudes bounds."""
+import numpy as np
+import pytest
+
+from oracle import mxref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU visible", allow_module_level=True)
+import bit_weight_only_dequant_amd as qgm  # noqa: E402
+
+DEV = "cuda:0"
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+TINY = {F16: 2.0 ** -24, BF16: 2.0 ** -133, F32: 2.0 ** -149}
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def check(y, ref, mag, K):
+    """ref rounded to y's type, within the bound of the head of this file."""
+    eps = torch.finfo(y.dtype).eps / 2
+    tol = eps * np.abs(ref) + TINY[y.dtype] / 2 + (1 + eps) * (K + 3) * 2.0 ** -23 * mag
+    err = np.abs(f64(y) - ref)
+    assert (err <= tol).all(), (np.unravel_index(np.argmax(err - tol), err.shape), (err / np.maximum(tol, 1e-300)).max())
+
+
+def rounded(ref, dtype):
+    """float64 (exact in fp32) rounded once to dtype, as float64."""
+    return f64(torch.from_numpy(np.asarray(ref, dtype=np.float32)).to(dtype))
+
+
+def random_mx(rng, R, K, spread=4, centre=122):
+    codes = rng.integers(0, 256, (R, K // 2), dtype=np.uint8)
+    return codes, rng.integers(centre - spread, centre + spread + 1, (R, K // 32)).astype(np.uint8)
+
+
+def make_x(rng, kind, M, K, exact=False):
+    """(device x, device x_scales, float64 values)."""
+    if kind == "mx":
+        c, s = random_mx(rng, M, K, spread=0 if exact else 6, centre=127)
+        return dev(c), dev(s), mxref.mx_values(c, s)
+    v = rng.integers(-4, 5, (M, K)) if exact else rng.standard_normal((M, K))
+    t = torch.from_numpy(v.astype(np.float32)).to(F16 if kind == "f16" else BF16)
+    return t.to(DEV), None, f64(t)
+
+
+XTYPE = {"f16": F16, "bf16": BF16}
+
+
+# ----------------------------------------------------- quantise and read back
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_quantize_every_pattern(dtype):
+    # every 16-bit pattern (for fp32: random patterns, subnormals and all
+    # exponents) beside a block's other values, finite blocks and others
+    rng = np.random.default_rng(3)
+    if dtype == F32:
+        x = torch.from_numpy(rng.integers(0, 1 << 32, (2048, 32), dtype=np.uint32).view(np.float32))
+        x[:512] = torch.from_numpy(rng.integers(0, 1 << 25, (512, 32), dtype=np.uint32).view(np.float32))
+    else:
+        bits = np.arange(65536, dtype=np.uint16)
+        x = torch.from_numpy(bits.view(np.int16).copy()).view(dtype).reshape(2048, 32)
+        x = torch.cat([x, x.reshape(32, 2048).t().contiguous()])
+    codes, scales = qgm.mx_quantize(x.to(DEV))
+    want_c, want_s = mxref.mx_quantize(x.double().numpy())
+    assert np.array_equal(scales.cpu().numpy(), want_s)
+    assert np.array_equal(codes.cpu().numpy(), want_c)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("M,K", [(1, 32), (3, 96), (257, 2080), (1, 8192), (70000, 32), (5, 64)])
+def test_quantize_sizes_and_strides(dtype, M, K):
+    rng = np.random.default_rng(M + K)
+    v = rng.standard_normal((M, K)) * np.exp2(rng.integers(-12, 12, (M, 1)))
+    v[rng.random((M, K)) < 0.2] *= 0.25   # ties' neighbourhood
+    v = np.round(v * 64) / 64
+    x = torch.from_numpy(v.astype(np.float32)).to(dtype)
+    want_c, want_s = mxref.mx_quantize(x.double().numpy())
+    wide = torch.full((M, K + 24), float("nan"), dtype=dtype, device=DEV)
+    wide[:, 8:8 + K] = x.to(DEV)
+    for t in (x.to(DEV), wide[:, 8:8 + K]):
+        codes = torch.full((M + 2, K // 2), 77, dtype=torch.uint8, device=DEV)
+        scales = torch.full((M + 2, K // 32), 77, dtype=torch.uint8, device=DEV)
+        qgm.mx_quantize(t, codes=codes[:M], scales=scales[:M])
+        assert np.array_equal(codes[:M].cpu().numpy(), want_c) and np.array_equal(scales[:M].cpu().numpy(), want_s)
+        assert bool((codes[M:] == 77).all()) and bool((scales[M:] == 77).all())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+def test_dequantize_every_scale_and_code(dtype):
+    scales = np.arange(256, dtype=np.uint8).reshape(256, 1)
+    nib = np.concatenate([np.arange(16), np.arange(15, -1, -1)]).astype(np.uint8)
+    codes = np.tile(nib[0::2] | nib[1::2] << 4, (256, 1)).astype(np.uint8)
+    y = qgm.mx_dequantize(dev(codes), dev(scales), dtype=dtype)
+    with np.errstate(over="ignore"):
+        ref = rounded(mxref.mx_values(codes, scales), dtype)
+    assert np.array_equal(f64(y), ref, equal_nan=True)
+
+
+def test_dequantize_strided_leaves_the_gap():
+    rng = np.random.default_rng(8)
+    codes, scales = random_mx(rng, 37, 160)
+    out = torch.full((37, 176), 5.0, dtype=F32, device=DEV)
+    qgm.mx_dequantize(dev(codes), dev(scales), out=out[:, 8:168])
+    assert np.array_equal(f64(out[:, 8:168]), mxref.mx_values(codes, scales))
+    assert bool((out[:, :8] == 5).all()) and bool((out[:, 168:] == 5).all())
+
+
+@pytest.mark.parametrize("M,K", [(0, 64), (4, 0)])
+def test_quantize_empty(M, K):
+    codes, scales = qgm.mx_quantize(torch.zeros(M, K, dtype=F16, device=DEV))
+    assert codes.shape == (M, K // 2) and scales.shape == (M, K // 32)
+    assert qgm.mx_dequantize(codes, scales).shape == (M, K)
+
+
+# ------------------------------------------------------------------ products
+
+SIZES = [(1, 1, 32), (1, 16, 64), (1, 250, 2048), (2, 17, 96), (7, 33, 160), (15, 64, 128), (16, 100, 288),
+         (17, 48, 512), (31, 16, 1056), (33, 130, 96), (63, 257, 256), (64, 128, 128), (65, 96, 544), (100, 65, 2080),
+         (127, 300, 32), (129, 129, 224), (200, 512, 384), (257, 200, 1024), (300, 777, 800), (513, 1030, 288),
+         (1100, 530, 416)]
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_gemm_exact_integers(kind, M, N, K):
+    # x integers to 4 (codes to 6, halves), weights with one scale: every partial
+    # sum is a multiple of 2^-7 below 2^17 (K 6 6 at most), exact in fp32
+    rng = np.random.default_rng(M * 7 + N + K)
+    x, xs, xv = make_x(rng, kind, M, K, exact=True)
+    wc, wsc = random_mx(rng, N, K, spread=0)
+    ref, _ = mxref.mx_gemm_ref(xv, mxref.mx_values(wc, wsc))
+    for yt in (F32, XTYPE.get(kind, F16)):
+        out = torch.full((M + 1, N), 9.0, dtype=yt, device=DEV)
+        y = qgm.mx_gemm(x, dev(wc), dev(wsc), x_scales=xs, out=out[:M])
+        assert np.array_equal(f64(y), rounded(ref, yt))
+        assert bool((out[M] == 9).all())
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("yt", [F16, BF16, F32])
+@pytest.mark.parametrize("M,N,K", [(1, 300, 2048), (5, 77, 96), (40, 129, 608), (130, 260, 1056), (600, 333, 512)])
+def test_gemm_random_with_residual_and_strides(kind, yt, M, N, K):
+    rng = np.random.default_rng(M + N * 3 + K)
+    x, xs, xv = make_x(rng, kind, M, K)
+    if xs is None:
+        wide = torch.full((M, K + 16), float("nan"), dtype=x.dtype, device=DEV)
+        wide[:, :K] = x
+        x = wide[:, :K]
+    wc, wsc = random_mx(rng, N, K)
+    r = torch.randn(M, N + 3, dtype=F32).to(yt)
+    out = torch.full((M, N + 5), 9.0, dtype=yt, device=DEV)
+    ref, mag = mxref.mx_gemm_ref(xv, mxref.mx_values(wc, wsc), residual=f64(r[:, :N]))
+    qgm.mx_gemm(x, dev(wc), dev(wsc), x_scales=xs, out=out[:, :N], residual=r.to(DEV)[:, :N])
+    check(out[:, :N], ref, mag, K)
+    assert bool((out[:, N:] == 9).all())
+    # in place: the residual is the output itself
+    y = r.to(DEV).contiguous()[:, :N].clone()
+    qgm.mx_gemm(x, dev(wc), dev(wsc), x_scales=xs, out=y, residual=y)
+    assert torch.equal(y, out[:, :N])
+
+
+@pytest.mark.parametrize("M", [1, 20, 150, 600])
+def test_gemm_f16_weights_beyond_f16(M):
+    # weights far below and above what fp16 can hold, in the same row as ordinary ones
+    rng = np.random.default_rng(M)
+    N, K = 70, 640
+    wc, wsc = random_mx(rng, N, K)
+    wsc[3, :] = 20       # 2^-107
+    wsc[4, 2] = 180      # 2^53
+    wsc[5, 7:9] = 95     # fp16 would keep some of the codes
+    wsc[6, ::2] = 141    # 6 * 2^14: past fp16's largest
+    x, _, xv = make_x(rng, "f16", M, K)
+    x[0, :4] = torch.tensor([65504.0, -65504.0, 2.0 ** -24, -(2.0 ** -24)], dtype=F16)
+    xv = f64(x)
+    ref, mag = mxref.mx_gemm_ref(xv, mxref.mx_values(wc, wsc))
+    check(qgm.mx_gemm(x, dev(wc), dev(wsc), out_dtype=F32), ref, mag, K)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("M,N,K", [(3, 40, 96), (70, 90, 416), (300, 270, 672)])
+def test_gemm_nan_and_inf_stay_in_their_row_and_column(kind, M, N, K):
+    rng = np.random.default_rng(M * N)
+    x, xs, xv = make_x(rng, kind, M, K)
+    wc, wsc = random_mx(rng, N, K)
+    wsc[5, -1] = 255
+    wsc[N - 1, 0] = 255
+    if kind == "mx":
+        xs[1, 0] = 255
+    else:
+        x[1, 3] = float("nan")
+        x[2, K - 1] = float("inf")
+    xv = mxref.mx_values(x.cpu().numpy(), xs.cpu().numpy()) if kind == "mx" else f64(x)
+    y = f64(qgm.mx_gemm(x, dev(wc), dev(wsc), x_scales=xs, out_dtype=F32))
+    with np.errstate(invalid="ignore"):
+        ref, _ = mxref.mx_gemm_ref(xv, mxref.mx_values(wc, wsc))
+        gap = np.abs(y - ref)
+    assert np.array_equal(np.isnan(y), np.isnan(ref)) and np.array_equal(np.isinf(y), np.isinf(ref))
+    ok = np.isfinite(ref)
+    ok_rows = [m for m in range(M) if np.isfinite(xv[m]).all()]
+    w0 = np.nan_to_num(mxref.mx_values(wc, wsc))
+    mag = np.abs(np.nan_to_num(xv, posinf=0)) @ np.abs(w0).T
+    assert (gap[ok_rows][ok[ok_rows]] <= ((K + 3) * 2.0 ** -23 * mag[ok_rows] + 2.0 ** -149)[ok[ok_rows]]).all()
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("M,N,K", [(1, 64, 8192), (64, 256, 1024), (512, 512, 1024)])
+def test_gemm_equal_inputs_give_equal_bits(kind, M, N, K):
+    rng = np.random.default_rng(5)
+    x, xs, _ = make_x(rng, kind, M, K)
+    w, ws = (dev(a) for a in random_mx(rng, N, K))
+    first = qgm.mx_gemm(x, w, ws, x_scales=xs, out_dtype=F32)
+    for _ in range(3):
+        assert torch.equal(first, qgm.mx_gemm(x, w, ws, x_scales=xs, out_dtype=F32))
+
+
+@pytest.mark.parametrize("M,N,K", [(0, 16, 64), (4, 0, 64), (3, 18, 0)])
+def test_gemm_empty(M, N, K):
+    w = torch.zeros(N, K // 2, dtype=torch.uint8, device=DEV)
+    ws = torch.zeros(N, K // 32, dtype=torch.uint8, device=DEV)
+    r = torch.randn(M, N, device=DEV).to(BF16)
+    for kind in ("bf16", "mx"):
+        x = torch.zeros(M, K, dtype=BF16, device=DEV) if kind == "bf16" else w.new_zeros(M, K // 2)
+        xs = None if kind == "bf16" else w.new_zeros(M, K // 32)
+        y = qgm.mx_gemm(x, w, ws, x_scales=xs, out_dtype=BF16, residual=r)
+        assert y.shape == (M, N) and (K > 0 or torch.equal(y, r))
+
+
+# ------------------------------------------------------------------- grouped
+
+def make_groups(sizes, head=0):
+    return np.concatenate([[head], head + np.cumsum(sizes)]).astype(np.int32)
+
+
+GROUPS = [[1], [3, 0, 5], [0, 0, 40], [16, 1, 0, 31], [1] * 20, [0, 200, 3], [130, 0, 70, 1, 64], [300, 260, 0, 513],
+          [5] * 70, [0, 0, 0]]
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("sizes", GROUPS, ids=lambda s: "-".join(map(str, s[:5])))
+@pytest.mark.parametrize("N,K", [(40, 96), (260, 544)])
+def test_grouped(kind, sizes, N, K):
+    rng = np.random.default_rng(sum(sizes) + N)
+    E, head, behind = len(sizes), 3, 2
+    off = make_groups(sizes, head)
+    T, xr = int(off[-1]) + behind, 50
+    rows = rng.integers(0, xr, T).astype(np.int32)     # rows chosen twice and never
+    rows[rng.random(T) < 0.1] = -1
+    rows[rng.random(T) < 0.05] = xr
+    scale = rng.standard_normal(T).astype(np.float32)
+    x, xs, xv = make_x(rng, kind, xr, K)
+    wc, wsc = random_mx(rng, E * N, K)
+    w, ws = dev(wc.reshape(E, N, -1)), dev(wsc.reshape(E, N, -1))
+    wv = mxref.mx_values(wc, wsc).reshape(E, N, K)
+    yt = XTYPE.get(kind, BF16)
+    out = torch.full((T, N), 9.0, dtype=yt, device=DEV)
+    qgm.mx_gemm_grouped(x, w, ws, dev(off), x_scales=xs, rows=dev(rows), row_scale=dev(scale), out=out)
+    ref, mag = mxref.mx_grouped_ref(xv, wv, off, rows, scale, fill=9.0)
+    check(out, ref, mag, K)
+    assert bool((out[:head] == 9).all()) and bool((out[T - behind:] == 9).all())
+    # rows in slot order, no factor
+    xt, xst, xtv = make_x(rng, kind, T, K)
+    out = torch.full((T, N), 9.0, dtype=F32, device=DEV)
+    qgm.mx_gemm_grouped(xt, w, ws, dev(off), x_scales=xst, out=out)
+    ref, mag = mxref.mx_grouped_ref(xtv, wv, off, fill=9.0)
+    check(out, ref, mag, K)
+
+
+@pytest.mark.parametrize("T", [9, 700])
+def test_grouped_one_group_is_the_plain_product(T):
+    rng = np.random.default_rng(T)
+    x, _, _ = make_x(rng, "bf16", T, 256)
+    w, ws = (dev(a) for a in random_mx(rng, 200, 256))
+    off = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    y, z = qgm.mx_gemm_grouped(x, w[None], ws[None], off, out_dtype=F32), qgm.mx_gemm(x, w, ws, out_dtype=F32)
+    mag = np.abs(f64(x)) @ np.abs(f64(qgm.mx_dequantize(w, ws, dtype=F32))).T
+    assert (np.abs(f64(y) - f64(z)) <= 2 * 259 * 2.0 ** -23 * mag).all()
+
+
+@pytest.mark.parametrize("kind", ["f16", "mx"])
+@pytest.mark.parametrize("T", [40, 400])
+@pytest.mark.parametrize("off", [[0, -5, 1000, 7], [9, 3, 3, 2], [-2147483648, 2147483647, 5, 2147483647]])
+def test_grouped_bad_offsets_stay_inside(kind, T, off):
+    # what the rows hold is unspecified; what lies around y is not touched
+    rng = np.random.default_rng(T)
+    N, K = 48, 160
+    x, xs, _ = make_x(rng, kind, T, K)
+    w, ws = (dev(a).reshape(3, N, -1) for a in random_mx(rng, 3 * N, K))
+    out = torch.full((T + 16, N), 9.0, dtype=F16, device=DEV)
+    qgm.mx_gemm_grouped(x, w, ws, torch.tensor(off, dtype=torch.int32, device=DEV), x_scales=xs, out=out[8:8 + T])
+    assert bool((out[:8] == 9).all()) and bool((out[8 + T:] == 9).all())
+
+
+def test_grouped_empty():
+    w, ws = torch.zeros(3, 16, 32, dtype=torch.uint8, device=DEV), torch.zeros(3, 16, 2, dtype=torch.uint8, device=DEV)
+    off = torch.zeros(4, dtype=torch.int32, device=DEV)
+    x = torch.zeros(0, 64, dtype=BF16, device=DEV)
+    assert qgm.mx_gemm_grouped(x, w, ws, off).shape == (0, 16)
+    # no rows of x at all, every slot without one: zeros
+    off[1:] = 5
+    rows = torch.full((5,), -1, dtype=torch.int32, device=DEV)
+    y = qgm.mx_gemm_grouped(x, w, ws, off, rows=rows, out=torch.full((5, 16), 9.0, dtype=BF16, device=DEV))
+    assert not bool(y.any())
+    # no experts: nothing is written
+    y = torch.full((4, 16), 9.0, dtype=BF16, device=DEV)
+    qgm.mx_gemm_grouped(x.new_zeros(4, 64), w[:0], ws[:0], off[:1], out=y)
+    assert bool((y == 9).all())
+
+
+# -------------------------------------------- as used together, graphs, streams
+
+def moe(x, up, down, offsets, rows, scale):
+    """An experts' block: 4-bit activations into the first product, a squared
+    ReLU, 16-bit ones into the second, the router's factor in its rounding."""
+    codes, scales = qgm.mx_quantize(x)
+    h = qgm.mx_gemm_grouped(codes, *up, offsets, x_scales=scales, rows=rows, out_dtype=BF16)
+    h = torch.relu(h) ** 2
+    return h, qgm.mx_gemm_grouped(h, *down, offsets, row_scale=scale)
+
+
+@pytest.mark.parametrize("tokens", [5, 300])
+def test_chain_and_its_graph(tokens):
+    rng = np.random.default_rng(tokens)
+    E, D, F, top = 6, 160, 288, 2
+    up, down = random_mx(rng, E * F, D), random_mx(rng, E * D, F)
+    dup = [dev(a).reshape(E, F, -1) for a in up]
+    ddn = [dev(a).reshape(E, D, -1) for a in down]
+    ids = rng.integers(0, E, tokens * top)
+    order = np.argsort(ids, kind="stable")
+    off = make_groups(np.bincount(ids, minlength=E))
+    rows = (order // top).astype(np.int32)
+    scale = rng.random(tokens * top).astype(np.float32)
+    x = torch.from_numpy(rng.standard_normal((tokens, D)).astype(np.float32)).to(DEV, BF16)
+    args = (dup, ddn, dev(off), dev(rows), dev(scale))
+    h, y = moe(x, *args)
+    xv = mxref.mx_values(*mxref.mx_quantize(f64(x)))
+    ref, mag = mxref.mx_grouped_ref(xv, mxref.mx_values(*up).reshape(E, F, D), off, rows)
+    pre = torch.from_numpy(np.maximum(ref, 0) ** 2)
+    # the first product's rounding passes through the square: compare h loosely, y from h itself
+    assert np.allclose(f64(h), pre.numpy(), rtol=2 ** -6, atol=1e-2 * float(mag.max()))
+    ref, mag = mxref.mx_grouped_ref(f64(h), mxref.mx_values(*down).reshape(E, D, F), off, row_scale=scale)
+    check(y, ref, mag, F)
+    static = x.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        moe(static, *args)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _, captured = moe(static, *args)
+    for i in range(4):
+        fresh = torch.from_numpy(rng.standard_normal((tokens, D)).astype(np.float32)).to(DEV, BF16)
+        _, eager = moe(fresh, *args)
+        static.copy_(fresh)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(captured, eager), i
+
+
+def test_products_on_a_named_stream():
+    rng = np.random.default_rng(0)
+    x, _, xv = make_x(rng, "f16", 40, 256)
+    wc, wsc = random_mx(rng, 96, 256)
+    w, ws = dev(wc), dev(wsc)
+    ref, mag = mxref.mx_gemm_ref(xv, mxref.mx_values(wc, wsc))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    lin = qgm.MXLinear(w, ws)
+    y = lin(x, stream=s)
+    z = qgm.mx_gemm_grouped(x, w[None], ws[None], torch.tensor([0, 40], dtype=torch.int32, device=DEV), stream=s)
+    c, sc = qgm.mx_quantize(x, stream=s)
+    v = qgm.mx_dequantize(c, sc, stream=s)
+    s.synchronize()
+    check(y, ref, mag, 256)
+    check(z, ref, mag, 256)
+    assert np.array_equal(f64(v), rounded(mxref.mx_values(*mxref.mx_quantize(xv)), F16))
+
+
+def test_binding_refuses():
+    x = torch.zeros(4, 64, dtype=F16, device=DEV)
+    w, ws = torch.zeros(8, 32, dtype=torch.uint8, device=DEV), torch.zeros(8, 2, dtype=torch.uint8, device=DEV)
+    off = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    xc, xs = w[:4], ws[:4]
+    bad = [
+        lambda: qgm.mx_quantize(x[:, :48]), lambda: qgm.mx_quantize(x.t()), lambda: qgm.mx_quantize(x.double()),
+        lambda: qgm.mx_quantize(x[0]), lambda: qgm.mx_quantize(x, codes=w), lambda: qgm.mx_quantize(x, scales=ws),
+        lambda: qgm.mx_dequantize(w, ws[:4]), lambda: qgm.mx_dequantize(w[:, ::2], ws),
+        lambda: qgm.mx_dequantize(w, ws, dtype=torch.int8), lambda: qgm.mx_dequantize(w, ws, out=x),
+        lambda: qgm.mx_gemm(x.float(), w, ws), lambda: qgm.mx_gemm(x[:, :32], w, ws),
+        lambda: qgm.mx_gemm(x, w.int(), ws), lambda: qgm.mx_gemm(x, w, ws[:, :1]), lambda: qgm.mx_gemm(x, w, ws.cpu()),
+        lambda: qgm.mx_gemm(xc, w, ws), lambda: qgm.mx_gemm(xc, w, ws, x_scales=xs[:3]),
+        lambda: qgm.mx_gemm(x, w, ws, x_scales=xs), lambda: qgm.mx_gemm(x, w, ws, out_dtype=torch.float64),
+        lambda: qgm.mx_gemm(x, w, ws, out=x), lambda: qgm.mx_gemm(x, w, ws, residual=x),
+        lambda: qgm.mx_gemm(x, w, ws, residual=torch.zeros(4, 8, device=DEV)),
+        lambda: qgm.mx_gemm(x, w, ws, out=torch.zeros(4, 8, device=DEV), out_dtype=F16),
+        lambda: qgm.mx_gemm_grouped(x, w, ws, off), lambda: qgm.mx_gemm_grouped(x, w[None], ws[None], off.long()),
+        lambda: qgm.mx_gemm_grouped(x, w[None], ws[None], off[:1]),
+        lambda: qgm.mx_gemm_grouped(x, w[None], ws[None], off, rows=off.float()),
+        lambda: qgm.mx_gemm_grouped(x, w[None], ws[None], off, rows=off, row_scale=torch.ones(3, device=DEV)),
+        lambda: qgm.mx_gemm_grouped(x, w[None], ws[None], off, row_scale=torch.ones(4, device=DEV, dtype=F16)),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(qgm.QGemmError):
+        qgm.mx_quantize(torch.zeros(4, 72, dtype=F16, device=DEV)[:, 4:68])   # rows not 16-byte aligned
