@@ -64,6 +64,7 @@ _SIGS = {
     "qmx_dequantize": ([_P, _P, _I, _I, _P, _I, _I, _P], _I),
     "qmx_gemm": ([_P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P], _I),
     "qmx_gemm_grouped": ([_P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _I, _I, _P, _I, _I, _P], _I),
+    "qmx_plan": ([_I, _I, _I, _I, _I, ctypes.POINTER(_I)], _I),
     "qg_stream_read": ([_P, _SZ, _P, _I, _P], _I),
     "qg_empty_launch": ([_I, _I, _P], _I),
     "qg_mfma_probe": ([_P, _I, _I, _P], _I),
@@ -626,6 +627,13 @@ def mx_gemm_grouped(x, w, w_scales, offsets, x_scales=None, rows=None, row_scale
                                      offsets.data_ptr(), E, T, _ptr(row_scale), N, K, y.data_ptr(), ldy, yt, s),
                "qmx_gemm_grouped")
     return y
+
+
+def mx_plan(M: int, N: int, K: int, x_type: int, groups: int = 0) -> dict:
+    """The kernel an MXFP4 product takes; see qmx_plan."""
+    out = (_I * 4)()
+    _check(_lib.qmx_plan(M, N, K, groups, x_type, out), "qmx_plan")
+    return dict(tile=out[0], blocks=out[1], waves=out[2], pieces=out[3])
 
 
 class MXLinear:

@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "../../include/qgemm.h"
 #include "internal.h"
@@ -25,6 +26,7 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef int i8v __attribute__((ext_vector_type(8)));
+typedef float f16v __attribute__((ext_vector_type(16)));
 
 constexpr int F16 = QG_MX_F16, BF16 = QG_MX_BF16, F32 = QG_MX_F32, FP4 = QG_MX_FP4;
 
@@ -150,7 +152,7 @@ struct MxArgs {
   const char* resid; char* y;
   int64_t ldx_bytes, ldr, ldy;      // x row pitch in bytes, the others in elements
   int x_rows, E, M, N, K;           // M: rows of y (the slots of a grouped product)
-  int y_type, vec;                  // vec: 4 consecutive outputs of a row may be stored at once
+  int y_type;
 };
 
 // 8 codes -> 8 exact 16-bit values (code times the block's scale)
@@ -202,54 +204,74 @@ __device__ __forceinline__ f4 mfma_fp4(u4 a, uint32_t sa, u4 b, uint32_t sb, f4 
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
-// Four consecutive outputs of one row: columns n .. n+3 of row m.
-__device__ __forceinline__ void store4(const MxArgs& a, int m, int n, f4 v, float rs) {
-  if (a.row_scale) {
+// S: which byte of the lanes' scale words counts
+template <int S> __device__ __forceinline__ f16v mfma_fp4_32(u4 a, uint32_t sa, u4 b, uint32_t sb, f16v c) {
+  const i8v av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  const i8v bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, S, (int)sa, S, (int)sb);
+}
+
+// C 16- or 32-bit values at element alignment, in vectors of up to 16 bytes
+template <int C, typename E> __device__ __forceinline__ void get(const E* p, E (&v)[C]) {
+  constexpr int B = C * sizeof(E) >= 16 ? 16 : 8;
+  typedef uint32_t vec __attribute__((ext_vector_type(B / 4), aligned(2)));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] *= rs;
+  for (int i = 0; i < (int)(C * sizeof(E)) / B; ++i) {
+    const vec t = reinterpret_cast<const vec*>(p)[i];
+    __builtin_memcpy(reinterpret_cast<char*>(v) + i * B, &t, B);
   }
-  const int64_t o = (int64_t)m * a.ldy + n, ro = (int64_t)m * a.ldr + n;
-  if (a.y_type == F32) {
-    float* y = reinterpret_cast<float*>(a.y);
-    const float* r = reinterpret_cast<const float*>(a.resid);
-    if (a.vec && n + 3 < a.N) {
-      if (r) v += *reinterpret_cast<const f4*>(r + ro);
-      *reinterpret_cast<f4*>(y + o) = v;
-    } else {
+}
+template <int C, typename E> __device__ __forceinline__ void put(E* p, const E (&v)[C]) {
+  constexpr int B = C * sizeof(E) >= 16 ? 16 : 8;
+  typedef uint32_t vec __attribute__((ext_vector_type(B / 4), aligned(2)));
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < a.N) y[o + i] = r ? v[i] + r[ro + i] : v[i];
+  for (int i = 0; i < (int)(C * sizeof(E)) / B; ++i) {
+    vec t;
+    __builtin_memcpy(&t, reinterpret_cast<const char*>(v) + i * B, B);
+    reinterpret_cast<vec*>(p)[i] = t;
+  }
+}
+
+// C (4 or 8) consecutive outputs of one row, columns n .. n+C-1 of row m: the
+// factor and the residual in fp32, one rounding.  Rows of any pitch are stored
+// in one piece (the device takes vector accesses at element alignment).
+template <int C> __device__ __forceinline__ void store_cols(const MxArgs& a, int m, int n, float (&v)[C], float rs) {
+  const int64_t o = (int64_t)m * a.ldy + n, ro = (int64_t)m * a.ldr + n;
+  const bool whole = n + C <= a.N;
+  const int have = min(a.N - n, C);
+#pragma unroll
+  for (int i = 0; i < C; ++i) v[i] *= rs;
+  if (a.y_type == F32) {
+    if (a.resid) {
+      float r[C] = {};
+      const float* rp = reinterpret_cast<const float*>(a.resid) + ro;
+      if (whole) get(rp, r);
+      else for (int i = 0; i < C; ++i) if (i < have) r[i] = rp[i];
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] += r[i];
     }
+    float* y = reinterpret_cast<float*>(a.y) + o;
+    if (whole) put(y, v);
+    else for (int i = 0; i < C; ++i) if (i < have) y[i] = v[i];
     return;
   }
-  uint16_t* y = reinterpret_cast<uint16_t*>(a.y);
-  const uint16_t* r = reinterpret_cast<const uint16_t*>(a.resid);
   const bool half = a.y_type == F16;
-  const bool wide = a.vec && n + 3 < a.N;
-  uint16_t rv[4] = {0, 0, 0, 0}, q[4];
-  if (r) {
-    if (wide) {
-      const u2 t = *reinterpret_cast<const u2*>(r + ro);
-      rv[0] = (uint16_t)t.x; rv[1] = (uint16_t)(t.x >> 16); rv[2] = (uint16_t)t.y; rv[3] = (uint16_t)(t.y >> 16);
-    } else {
+  if (a.resid) {
+    uint16_t r[C] = {};
+    const uint16_t* rp = reinterpret_cast<const uint16_t*>(a.resid) + ro;
+    if (whole) get(rp, r);
+    else for (int i = 0; i < C; ++i) if (i < have) r[i] = rp[i];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < a.N) rv[i] = r[ro + i];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] += half ? (float)__builtin_bit_cast(f16, rv[i]) : bits_f32((uint32_t)rv[i] << 16);
+    for (int i = 0; i < C; ++i)
+      v[i] += half ? (float)__builtin_bit_cast(f16, r[i]) : bits_f32((uint32_t)r[i] << 16);
   }
+  uint16_t q[C];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < C; ++i)
     q[i] = half ? __builtin_bit_cast(uint16_t, (f16)v[i]) : __builtin_bit_cast(uint16_t, (bf16)v[i]);
-  if (wide) {
-    *reinterpret_cast<u2*>(y + o) = u2{q[0] | ((uint32_t)q[1] << 16), q[2] | ((uint32_t)q[3] << 16)};
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < a.N) y[o + i] = q[i];
-  }
+  uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + o;
+  if (whole) put(y, q);
+  else for (int i = 0; i < C; ++i) if (i < have) y[i] = q[i];
 }
 
 // A grouped product's slots of expert e, kept within [0, T] whatever the
@@ -259,119 +281,696 @@ __device__ __forceinline__ void group_bounds(const MxArgs& a, int e, int& begin,
   end = min(max(a.offsets[e + 1], begin), a.M);
 }
 
-// Few rows: bound by the weights' bytes.  A workgroup owns 16 columns of y (16
-// rows of W) and 16*MT rows of it; its NW waves share K in tiles of 128 and
-// are summed through LDS in wave order.  Lane l = 16 g + r of a wave loads the
-// 16-byte block 4 t + g of row r (with its scale byte), which is the operand of
-// v_mfma_scale_f32_16x16x128 as it is; 16-bit x takes four 16x16x32 steps on
-// the block's four words converted to 16 bits, x read at the same k.  W is the
-// first operand, so a lane ends with four consecutive outputs of one row.
-template <int XT, int MT, int NW, bool GROUPED>
+// The row of x that slot m reads: its own where it has one, else some row of x
+// (the outputs of such a slot are not stored, or stored as zeros).
+template <bool GROUPED> __device__ __forceinline__ int x_row(const MxArgs& a, int m, int m_end) {
+  m = min(m, m_end - 1);
+  if (GROUPED && a.rows) m = a.rows[m];
+  return m >= 0 && m < a.x_rows ? m : 0;
+}
+
+// Whether slot m has a row of x at all.
+template <bool GROUPED> __device__ __forceinline__ bool has_row(const MxArgs& a, int m) {
+  if (!GROUPED || !a.rows) return true;
+  m = a.rows[m];
+  return m >= 0 && m < a.x_rows;
+}
+
+typedef const void __attribute__((address_space(1)))* gptr;
+typedef void __attribute__((address_space(3)))* lptr;
+
+// At most N of this wave's global loads are on their way, and none of its LDS
+// reads (s_waitcnt vmcnt(N) lgkmcnt(0), GFX9 encoding).
+template <int N> __device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+
+// Few rows: bound by the weights' bytes, and next to them by the number of
+// vector loads (one takes a CU's address unit about 16 cycles however little it
+// brings).  A workgroup owns 16*NT columns of y (rows of W) and up to 16 rows
+// of it; its NW waves take K's chunks of 512 in turn and are summed through LDS
+// in wave order.  Lane l = 16 g + r of a wave loads the four 16-byte blocks
+// 4 u + g of a chunk of row r, which are the operand of
+// v_mfma_scale_f32_16x16x128 as they are, and the row's 16 scale bytes at once;
+// 16-bit x takes four 16x16x32 steps on a block's four words converted to 16
+// bits.  x goes straight to the wave's own LDS, a kilobyte a load and no more
+// rows than there are; row r keeps its 16-byte chunk c at place c ^ r, so 16
+// rows' reads touch the 64 banks once.  A workgroup goes through its share of
+// the column blocks (every gridDim.x-th), the next block's weights on their way
+// while one is multiplied and summed; where every wave has one chunk, x stays.
+// W is the first operand, so a lane ends with four consecutive outputs of one
+// row.
+
+// A barrier that waits for LDS accesses only: loads stay on their way.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+  asm volatile("" ::: "memory");        // no LDS access moves across the barrier
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// LDS of a wave for a chunk of x: whole direct loads of a kilobyte (four MXFP4 rows, one 16-bit row)
+template <int XT> __host__ __device__ constexpr int rows_x_bytes(int M) {
+  const int rows = M < 16 ? M : 16;
+  return 1024 * (XT == FP4 ? (rows + 3) / 4 : rows);
+}
+
+template <int XT, int NT, int NW, bool SHORT, bool MULTI, bool GROUPED>
 __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
-  __shared__ f4 part[NW][MT][64];
+  constexpr int XC = XT == FP4 ? 256 : 1024;     // bytes of an x row a chunk
+  const int xbytes = rows_x_bytes<XT>(a.M);      // a wave's part of the LDS
+  extern __shared__ __align__(1024) uint8_t rows_lds[];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n0 = blockIdx.x * 16;
   const int nkb = a.x_rows > 0 ? a.K >> 5 : 0;   // no x to read: all rows are zero
-  const int tiles = (nkb + 3) >> 2;
+  const int chunks = (nkb + 15) >> 4, turns = (chunks + NW - 1) / NW;   // a wave's chunks: wave, wave + NW, ..
+  const int blocks = (a.N + 16 * NT - 1) / (16 * NT);
   int m_begin, m_end;
-  int64_t wrow = min(n0 + r, a.N - 1);
   if constexpr (GROUPED) {
     group_bounds(a, blockIdx.y, m_begin, m_end);
-    wrow += (int64_t)blockIdx.y * a.N;
   } else {
-    m_begin = blockIdx.y * (16 * MT);
-    m_end = min(a.M, m_begin + 16 * MT);
+    m_begin = blockIdx.y * 16;
+    m_end = min(a.M, m_begin + 16);
   }
-  const uint8_t* wp = a.w + wrow * (a.K >> 1);
-  const uint8_t* sp = a.ws + wrow * (a.K >> 5);
-  for (int m0 = m_begin; m0 < m_end; m0 += 16 * MT) {
-    const char* xp[MT];
-    const uint8_t* xsp[MT];
+  // 16 scale bytes of a row from block 16 c on (a row's last ones at most), or
+  // where K < 512 the lane's own four, one a word.  scale_words() puts them in
+  // place when they are used: doing so at once would wait for the load.
+  auto load_scales = [&](const uint8_t* p, int c) {
+    typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(1)));
+    u4 v;
+    if constexpr (!SHORT) {
+      v = *reinterpret_cast<const vec*>(p + min(c * 16, nkb - 16));
+    } else {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      int m = min(m0 + mt * 16 + r, m_end - 1);
-      if (GROUPED && a.rows) m = a.rows[m];
-      if (m < 0 || m >= a.x_rows) m = 0;         // such a row's sums are not used
-      xp[mt] = a.x + m * a.ldx_bytes;
-      xsp[mt] = XT == FP4 ? a.xs + (int64_t)m * (a.K >> 5) : nullptr;
+      for (int u = 0; u < 4; ++u) v[u] = p[min(4 * u + g, nkb - 1)];
     }
-    f4 acc[MT];
+    return v;
+  };
+  auto scale_words = [&](u4 v, int c) {   // word u: the four scale bytes of blocks 4 u .. 4 u + 3, this lane's first
+    if constexpr (SHORT) return v;
+    const int sh = 8 * max(c * 16 - (nkb - 16), 0);
+    if (sh) {
+      const uint64_t lo = v.x | ((uint64_t)v.y << 32), hi = v.z | ((uint64_t)v.w << 32);
+      const uint64_t l = sh >= 64 ? hi >> (sh - 64) : (lo >> sh) | (hi << (64 - sh));
+      const uint64_t u = sh >= 64 ? 0 : hi >> sh;
+      v = u4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)u, (uint32_t)(u >> 32)};
+    }
+    return u4{v.x >> (8 * g), v.y >> (8 * g), v.z >> (8 * g), v.w >> (8 * g)};
+  };
+  constexpr int WLOADS = NT * (SHORT ? 8 : 5);   // loads of load_w
+  struct W { u4 c[NT][4], s[NT]; };
+  auto load_w = [&](int nb, int c, W& w) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt] = f4{0.f, 0.f, 0.f, 0.f};
-    for (int t = wave; t < tiles; t += NW) {
-      const bool in = 4 * t + g < nkb;           // past K: zero codes, zero x
-      const int kb = min(4 * t + g, nkb - 1);
-      u4 c = *reinterpret_cast<const u4*>(wp + kb * 16);
-      uint32_t s = sp[kb];
-      if (!in) c = u4{0, 0, 0, 0}, s = 127;
-      const float sf = scale_f32(s);
+    for (int j = 0; j < NT; ++j) {
+      const int64_t row = (GROUPED ? (int64_t)blockIdx.y * a.N : 0) + min((nb * NT + j) * 16 + r, a.N - 1);
+      const uint8_t* wp = a.w + row * (a.K >> 1);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        w.c[j][u] = *reinterpret_cast<const u4*>(wp + (int64_t)min(c * 16 + 4 * u + g, nkb - 1) * 16);
+      w.s[j] = load_scales(a.ws + row * (a.K >> 5), c);
+    }
+  };
+  auto dma = [](const char* from, uint8_t* to) { __builtin_amdgcn_global_load_lds((gptr)from, (lptr)to, 16, 0, 0); };
+  uint8_t* const xl = rows_lds + wave * xbytes;
+
+  for (int m0 = m_begin; m0 < m_end; m0 += 16) {
+    // what belongs to row m0 + r is loaded first, so that no later wait is for it
+    const int rows = min(16, m_end - m0), rr = min(r, rows - 1);
+    const int xr = x_row<GROUPED>(a, m0 + r, m_end);
+    const bool has = has_row<GROUPED>(a, m0 + rr);
+    const float factor = GROUPED && a.row_scale ? a.row_scale[m0 + rr] : 1.f;
+    // x: a whole chunk of the rows there are (past K: a row's last piece again)
+    auto load_x = [&](int c) {
       if constexpr (XT == FP4) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          u4 xc = *reinterpret_cast<const u4*>(xp[mt] + kb * 16);
-          uint32_t xsc = xsp[mt][kb];
-          if (!in) xc = u4{0, 0, 0, 0}, xsc = 127;
-          acc[mt] = mfma_fp4(c, s, xc, xsc, acc[mt]);
+        for (int i = 0; i < rows; i += 4) {
+          const int row = i + (lane >> 4);
+          dma(a.x + __shfl(xr, row) * a.ldx_bytes + (int64_t)min(c * 16 + ((lane & 15) ^ row), nkb - 1) * 16, xl + i * XC);
         }
       } else {
-        u4 xv[MT][4];
+        for (int i = 0; i < rows; ++i)
+          dma(a.x + __builtin_amdgcn_readlane(xr, i) * a.ldx_bytes + (int64_t)min(c * 64 + (lane ^ i), nkb * 4 - 1) * 16,
+              xl + i * XC);
+      }
+    };
+    u4 xs = {0, 0, 0, 0};
+    f4 acc[NT];
+    int nb = blockIdx.x, turn = 0, buf = 0;
+    const uint8_t* const xsp = XT == FP4 ? a.xs + (int64_t)xr * (a.K >> 5) : nullptr;
+    if (turns == 1 && wave < chunks) {
+      load_x(wave);
+      if constexpr (XT == FP4) xs = load_scales(xsp, wave);
+    }
+    // one chunk of one block: its products, and after a block's last chunk the sums
+    auto item = [&](auto MORE, W& w, W& next) {   // MORE: another item follows
+      const int c = wave + turn * NW;
+      const bool last = turn + 1 >= turns;
+      if (turns > 1 && c < chunks) {
+        load_x(c);
+        if constexpr (XT == FP4) xs = load_scales(xsp, c);
+      }
+      // the next item's weights (a wave without a chunk loads some); all loads but those are waited for
+      if constexpr (decltype(MORE)::value) {
+        load_w(last ? nb + (int)gridDim.x : nb, min(last ? wave : c + NW, chunks - 1), next);
+        wait_loads<WLOADS>();
+      } else {
+        wait_loads<0>();
+      }
+      if (turn == 0) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int j = 0; j < NT; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
+      }
+      if (c < chunks) {
+        u4 ws[NT];
+        bool fits = true;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            xv[mt][j] = reinterpret_cast<const u4*>(xp[mt] + kb * 64)[j];
-            if (!in) xv[mt][j] = u4{0, 0, 0, 0};
+        for (int j = 0; j < NT; ++j) {
+          ws[j] = scale_words(w.s[j], c);
+          if constexpr (XT == F16) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) fits = fits && (c * 16 + 4 * u + g >= nkb || scale_fits_f16(ws[j][u] & 255));
           }
-        if constexpr (XT == BF16) {
+        }
+        if constexpr (XT == F16) fits = __all(fits);
+        const u4 xw = scale_words(xs, c);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const b8 wv = codes_bf16(c[j], sf);
+        for (int u = 0; u < 4; ++u) {
+          if (c * 16 + 4 * u >= nkb) break;
+          const bool past = c * 16 + 4 * u + g >= nkb;   // zero operands, factor 1
+          uint32_t s[NT];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(b8, xv[mt][j]), acc[mt], 0, 0, 0);
+          for (int j = 0; j < NT; ++j) {
+            s[j] = past ? 127u : ws[j][u] & 255;
+            if (past) w.c[j][u] = u4{0, 0, 0, 0};
           }
-        } else if (__all(scale_fits_f16(s))) {
+          if constexpr (XT == FP4) {
+            u4 xv = *reinterpret_cast<const u4*>(xl + rr * XC + (((4 * u + g) ^ rr) * 16));
+            if (past) xv = u4{0, 0, 0, 0};
+            const uint32_t xsc = past ? 127u : xw[u];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const h8 wv = codes_f16(c[j], sf);
+            for (int j = 0; j < NT; ++j) acc[j] = mfma_fp4(w.c[j][u], s[j], xv, xsc, acc[j]);
+          } else {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, __builtin_bit_cast(h8, xv[mt][j]), acc[mt], 0, 0, 0);
-          }
-        } else {   // scales beyond fp16's range: bf16 weights, x in two exact parts
+            for (int q = 0; q < 4; ++q) {
+              u4 xv = *reinterpret_cast<const u4*>(xl + rr * XC + (((16 * u + 4 * g + q) ^ rr) * 16));
+              if (past) xv = u4{0, 0, 0, 0};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const b8 wv = codes_bf16(c[j], sf);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              b8 hi, lo;
-              split_f16(__builtin_bit_cast(h8, xv[mt][j]), hi, lo);
-              acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, hi, acc[mt], 0, 0, 0);
-              acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, lo, acc[mt], 0, 0, 0);
+              for (int j = 0; j < NT; ++j) {
+                if constexpr (XT == BF16) {
+                  acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(w.c[j][u][q], scale_f32(s[j])),
+                                                                   __builtin_bit_cast(b8, xv), acc[j], 0, 0, 0);
+                } else if (fits) {
+                  acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(w.c[j][u][q], scale_f32(s[j])),
+                                                                  __builtin_bit_cast(h8, xv), acc[j], 0, 0, 0);
+                } else {   // beyond fp16's range: bf16 weights, x in two exact parts
+                  const b8 wv = codes_bf16(w.c[j][u][q], scale_f32(s[j]));
+                  b8 hi, lo;
+                  split_f16(__builtin_bit_cast(h8, xv), hi, lo);
+                  acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, hi, acc[j], 0, 0, 0);
+                  acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, lo, acc[j], 0, 0, 0);
+                }
+              }
             }
           }
         }
       }
-    }
-    if (m0 != m_begin) __syncthreads();          // the last chunk's sums have been read
+      if (!last) {
+        __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): x has been read, its place may be sent for again
+        asm volatile("" ::: "memory");
+        ++turn;
+        return;
+      }
+      // the waves' sums; two buffers, so one barrier a block does
+      f4* part = reinterpret_cast<f4*>(rows_lds + NW * xbytes) + buf * (NW * NT * 64);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) part[wave][mt][lane] = acc[mt];
-    __syncthreads();
-    for (int mt = wave; mt < MT; mt += NW) {
-      f4 v = part[0][mt][lane];
+      for (int j = 0; j < NT; ++j) part[(wave * NT + j) * 64 + lane] = acc[j];
+      lds_barrier();
 #pragma unroll
-      for (int w = 1; w < NW; ++w) v += part[w][mt][lane];
-      const int m = m0 + mt * 16 + r, n = n0 + 4 * g;
-      if (m < m_end && n < a.N) {
-        if (GROUPED && a.rows) {
-          const int xr = a.rows[m];
-          if (xr < 0 || xr >= a.x_rows) v = f4{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < NT; ++j) {
+        if (wave != (buf * NT + j) % NW) continue;   // the waves take the sums in turn
+        f4 v = part[j * 64 + lane];
+#pragma unroll
+        for (int k = 1; k < NW; ++k) v += part[(k * NT + j) * 64 + lane];
+        const int m = m0 + r, n = (nb * NT + j) * 16 + 4 * g;
+        if (m < m_end && n < a.N) {
+          if (!has) v = f4{0.f, 0.f, 0.f, 0.f};
+          float o[4] = {v.x, v.y, v.z, v.w};
+          store_cols<4>(a, m, n, o, factor);
         }
-        store4(a, m, n, v, GROUPED && a.row_scale ? a.row_scale[m] : 1.f);
+      }
+      buf ^= 1;
+      turn = 0;
+      nb += gridDim.x;
+    };
+    W w0, w1;
+    int left = nb < blocks ? ((blocks - 1 - nb) / (int)gridDim.x + 1) * max(turns, 1) : 0;
+    if (chunks > 0) load_w(nb, min(wave, chunks - 1), w0);
+    if constexpr (MULTI) {
+      for (; left > 2; left -= 2) {
+        item(std::true_type{}, w0, w1);
+        item(std::true_type{}, w1, w0);
+      }
+      if (left == 2) {
+        item(std::true_type{}, w0, w1);
+        item(std::false_type{}, w1, w0);
+        left = 0;
       }
     }
+    if (left == 1) item(std::false_type{}, w0, w1);
+    lds_barrier();   // the sums have been read before the next 16 rows' are written
   }
+}
+
+// ---------------------------------------------------------------------------
+// many rows, both sides MXFP4
+// ---------------------------------------------------------------------------
+// Where a workgroup's tile lies: group e, rows m0 .. m_end of y (at most TM of
+// them), column tile tn.  Returns false when there is no tile for it.
+// Tiles are numbered n fastest within blocks of 8 row tiles, and a number range
+// goes to one XCD (workgroup b runs on XCD b % 8), so the tiles whose operands
+// an XCD's L2 holds run together.  A grouped product finds its row tiles from
+// the offsets: lane by lane the tiles of 64 groups, a running sum, a vote.
+struct Tile { int e, m0, m_end, tn; };
+
+template <int TM, bool GROUPED>
+__device__ __forceinline__ bool find_tile(const MxArgs& a, int tiles_n, Tile& t) {
+  int tiles_m = 0;
+  const int lane = threadIdx.x & 63;
+  if constexpr (GROUPED) {
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+      int n = 0;
+      if (e0 + lane < a.E) {
+        int b, e;
+        group_bounds(a, e0 + lane, b, e);
+        n = (e - b + TM - 1) / TM;
+      }
+#pragma unroll
+      for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d);
+      tiles_m += n;
+    }
+  } else {
+    tiles_m = (a.M + TM - 1) / TM;
+  }
+  const int64_t total = (int64_t)tiles_m * tiles_n;
+  const int xcd = blockIdx.x & 7;
+  const int64_t lo = total * xcd / 8, hi = total * (xcd + 1) / 8;
+  const int64_t id = lo + (blockIdx.x >> 3);
+  if (id >= hi) return false;
+  const int64_t per = (int64_t)8 * tiles_n;
+  const int blk = (int)(id / per), in = (int)(id - blk * per);
+  const int bm = min(8, tiles_m - blk * 8);
+  int tm = blk * 8 + in % bm;
+  t.tn = in / bm;
+  t.e = 0;
+  if constexpr (GROUPED) {
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+      int n = 0, b = 0, e = 0;
+      if (e0 + lane < a.E) {
+        group_bounds(a, e0 + lane, b, e);
+        n = (e - b + TM - 1) / TM;
+      }
+      int sum = n;   // tiles of the groups up to and with this lane's
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(sum, d);
+        if (lane >= d) sum += v;
+      }
+      const uint64_t vote = __ballot(sum > tm);
+      if (vote) {
+        const int who = __builtin_ctzll(vote);
+        t.e = e0 + who;
+        t.m0 = __shfl(b, who) + (tm - __shfl(sum - n, who)) * TM;
+        t.m_end = min(__shfl(e, who), t.m0 + TM);
+        return true;
+      }
+      tm -= __shfl(sum, 63);
+    }
+    return false;
+  }
+  t.m0 = tm * TM;
+  t.m_end = min(a.M, t.m0 + TM);
+  return true;
+}
+
+
+// Stores a wave's MI x NI blocks of 32 x 32 (element 4 q + k of lane 32 h + r:
+// column 8 q + 4 h + k, row r) at rows row0 of the tile and column n0.  Each
+// strip of 32 rows passes through LDS (the wave's own `strip`, rows padded by
+// 16 bytes), so that a lane stores 8 consecutive outputs and 4 NI lanes a
+// contiguous row piece.
+template <int MI, int NI, bool GROUPED>
+__device__ __forceinline__ void store_blocks(const MxArgs& a, const Tile& t, uint8_t* strip, int row0, int n0,
+                                             const f16v (&acc)[MI][NI]) {
+  constexpr int PITCH = 32 * NI + 4, LANES = 4 * NI, ROWS = 64 / LANES;
+  const int lane = threadIdx.x & 63;
+  float* s = reinterpret_cast<float*>(strip);
+  __syncthreads();                                   // every wave has read its last stage
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f4*>(s + (lane & 31) * PITCH + 32 * j + 8 * q + 4 * (lane >> 5)) =
+            f4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const int n = n0 + (lane % LANES) * 8;
+#pragma unroll 1
+    for (int r = lane / LANES; r < 32; r += ROWS) {
+      const int m = t.m0 + row0 + i * 32 + r;
+      if (m >= t.m_end || n >= a.N) continue;
+      float v[8];
+      __builtin_memcpy(v, s + r * PITCH + (lane % LANES) * 8, sizeof(v));
+      if (!has_row<GROUPED>(a, m)) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = 0.f;
+      }
+      store_cols<8>(a, m, n, v, GROUPED && a.row_scale ? a.row_scale[m] : 1.f);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+// A 32 x 32 x 16 product of 16-bit operands.
+__device__ __forceinline__ f16v mfma_16(b8 a, b8 b, f16v c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f16v mfma_16(h8 a, h8 b, f16v c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+
+// x and W stream through a ring of RING LDS stages of 128 k: a workgroup of WM
+// x WN waves, each MI x NI blocks of 32 x 32 outputs.  The loads go straight to
+// LDS, RING - 1 stages ahead.  A row's 16-byte chunks change places by the
+// row's number, so that the fragment reads of 16 consecutive rows touch the 64
+// banks once: MXFP4 rows are 64 bytes (chunk c at c ^ (row / 4 % 4)), 16-bit
+// rows 256 (c ^ (row % 16)).  A stage is two steps of 64 k, lane half h taking
+// the 32-block h of a step: with MXFP4 x one scaled matrix instruction a
+// block, with 16-bit x four of 16 k on the weights' words converted to 16 bits.
+// The fragments of one step are read while the other's are multiplied.  The
+// one barrier a stage, in between, says both that everyone's loads of the next
+// stage have arrived and that this stage has been read.  Every stage issues the
+// same loads, so a count of the outstanding ones tells which have arrived.  W
+// is the first operand of the matrix instruction: a lane's outputs run along a
+// row of y.
+template <int XT, int MI, int NI, int WM, int WN, int RING, bool GROUPED>
+__global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int tiles_n) {
+  constexpr int NW = WM * WN, TM = 32 * MI * WM, TN = 32 * NI * WN;
+  constexpr bool FP = XT == FP4;
+  constexpr int XB = FP ? 64 : 256, XR = 1024 / XB;        // bytes of an x row a stage, rows a direct load brings
+  constexpr int QA = TM / XR / NW, QB = TN / 16 / NW, QD = QA + QB;   // direct loads of 1 KiB a wave and stage
+  static_assert(QA * XR * NW == TM && QB * 16 * NW == TN, "rows split evenly over the waves");
+  constexpr int SROWS = FP ? TM + TN : TN, SOFF = FP ? TM : 0;   // rows with scales; W's first
+  constexpr int STAGE = TM * XB + TN * 64;
+  static_assert(SROWS % 64 == 0 && SROWS / 64 <= NW, "a wave brings the scales of 64 rows");
+  static_assert(NW * 32 * (32 * NI + 4) * 4 <= RING * STAGE, "store_blocks' strips");
+  // one array: with two, the compiler waits for every direct load before each read
+  __shared__ __align__(1024) uint8_t smem[RING * STAGE + 2 * SROWS * 16];
+  uint8_t* const sc = smem + RING * STAGE;   // scales: two groups of four stages, 16 bytes a row
+  Tile t;
+  if (!find_tile<TM, GROUPED>(a, tiles_n, t)) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int n0 = t.tn * TN;
+  const int nkb = a.K >> 5;
+
+  // direct loads: lane l brings a 16-byte chunk of row l / 4 of 16 (16-bit x: row l / 16 of 4)
+  const char* src[QD];
+#pragma unroll
+  for (int q = 0; q < QA; ++q)
+    src[q] = a.x + x_row<GROUPED>(a, t.m0 + (wave * QA + q) * XR + lane / (64 / XR), t.m_end) * a.ldx_bytes;
+#pragma unroll
+  for (int q = 0; q < QB; ++q)
+    src[QA + q] = reinterpret_cast<const char*>(a.w) +
+                  ((int64_t)t.e * a.N + min(n0 + (wave * QB + q) * 16 + (lane >> 2), a.N - 1)) * (a.K >> 1);
+  // scales: the 16 bytes of a group of stages of row l of 64 (waves to spare bring the same rows again)
+  const int swave = wave % (SROWS / 64);
+  const uint8_t* ssrc;
+  {
+    const int r = swave * 64 + lane;
+    ssrc = FP && r < TM ? a.xs + (int64_t)x_row<GROUPED>(a, t.m0 + r, t.m_end) * nkb
+                        : a.ws + ((int64_t)t.e * a.N + min(n0 + r - SOFF, a.N - 1)) * nkb;
+  }
+  // fragments: lane l reads row l % 32, MXFP4 chunk 2 s + l / 32 of step s, 16-bit chunks 8 s + 4 (l / 32) + 0..3
+  const int fr = lane & 31, h = lane >> 5;
+  uint32_t foff[2], xoff[2][4];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    foff[s] = fr * 64 + (((2 * s + h) ^ ((fr >> 2) & 3)) * 16);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) xoff[s][c] = fr * 256 + (((8 * s + 4 * h + c) ^ (fr & 15)) * 16);
+  }
+  f16v acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.f;
+
+  auto dma = [](const char* from, uint8_t* to) { __builtin_amdgcn_global_load_lds((gptr)from, (lptr)to, 16, 0, 0); };
+  auto issue = [&](int it, uint8_t* to, int q) {   // past the end: the rows' last chunk, into a place that is not read any more
+    if (FP || q >= QA) {
+      const int off = min(it * 4 + ((lane & 3) ^ (lane >> 4)), nkb - 1) * 16;
+      dma(src[q] + off, to + (q < QA ? (wave * QA + q) * 1024 : TM * XB + (wave * QB + q - QA) * 1024));
+    } else {
+      const int c = ((lane & 15) ^ (lane >> 4)) ^ (4 * ((wave * QA + q) & 3));
+      dma(src[q] + (int64_t)min(it * 16 + c, nkb * 4 - 1) * 16, to + (wave * QA + q) * 1024);
+    }
+  };
+  auto issue_scales = [&](int group) {   // the row's last 16 bytes at most
+    dma(reinterpret_cast<const char*>(ssrc) + min(group * 16, nkb - 16), sc + (group & 1) * (SROWS * 16) + swave * 1024);
+  };
+  auto barrier = [] {
+    asm volatile("" ::: "memory");   // no LDS access moves across it
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  struct Frag { u4 a[MI][FP ? 1 : 4], b[NI]; };
+  auto read = [&](const uint8_t* from, int s) {
+    Frag f;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) f.b[j] = *reinterpret_cast<const u4*>(from + TM * XB + (wn * NI + j) * 2048 + foff[s]);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int c = 0; c < (FP ? 1 : 4); ++c)
+        f.a[i][c] = *reinterpret_cast<const u4*>(from + (wm * MI + i) * 32 * XB + (FP ? foff[s] : xoff[s][c]));
+    return f;
+  };
+  // the scale words of a stage: byte 0 and byte 2 are this lane half's blocks of the two steps
+  struct Scales { uint32_t a[FP ? MI : 1], b[NI]; };
+  // the products of one step; `between` runs after each of MI * NI parts
+  auto multiply = [&](auto S, const Frag& f, const Scales& w, auto between) {
+    constexpr int s = decltype(S)::value;
+    if constexpr (FP) {
+#pragma unroll
+      for (int k = 0; k < MI * NI; ++k) {
+        const int i = k / NI, j = k % NI;
+        acc[i][j] = mfma_fp4_32<2 * s>(f.b[j], w.b[j], f.a[i][0], w.a[i], acc[i][j]);
+        between(k);
+      }
+    } else {
+      float sf[NI];
+#pragma unroll
+      for (int j = 0; j < NI; ++j) sf[j] = scale_f32((w.b[j] >> (16 * s)) & 255);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if constexpr (XT == F16) {
+          h8 wv[NI];
+#pragma unroll
+          for (int j = 0; j < NI; ++j) wv[j] = codes_f16(f.b[j][c], sf[j]);
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) acc[i][j] = mfma_16(wv[j], __builtin_bit_cast(h8, f.a[i][c]), acc[i][j]);
+        } else {
+          b8 wv[NI];
+#pragma unroll
+          for (int j = 0; j < NI; ++j) wv[j] = codes_bf16(f.b[j][c], sf[j]);
+#pragma unroll
+          for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) acc[i][j] = mfma_16(wv[j], __builtin_bit_cast(b8, f.a[i][c]), acc[i][j]);
+        }
+        // between() MI * NI times in all, spread over the four words
+#pragma unroll
+        for (int k = 0; k < MI * NI; ++k)
+          if (k * 4 / (MI * NI) == c) between(k);
+      }
+    }
+  };
+  auto nothing = [](int) {};
+  // fp16 x and weights beyond fp16's range: a stage on bf16 weights and x in two
+  // exact parts, operands taken from LDS as they are needed.  The row's scale
+  // bytes at `scales` begin with block `first`.
+  auto wide_stage = [&](int it, const uint8_t* place, const uint8_t* scales, int first) {
+#pragma unroll 1
+    for (int n = 0; n < 8; ++n) {
+      const int s = n >> 2, c = n & 3, kb = it * 4 + 2 * s + h;
+      b8 wv[NI];
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const int row = (wn * NI + j) * 32 + fr;
+        const uint8_t* p = place + TM * XB + row * 64 + (((2 * s + h) ^ ((fr >> 2) & 3)) * 16) + 4 * c;
+        const uint32_t word = kb < nkb ? *reinterpret_cast<const uint32_t*>(p) : 0u;
+        wv[j] = codes_bf16(word, kb < nkb ? scale_f32(scales[row * 16 + kb - first]) : 1.f);
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const uint8_t* p = place + ((wm * MI + i) * 32 + fr) * XB + (((8 * s + 4 * h + c) ^ (fr & 15)) * 16);
+        h8 xv = *reinterpret_cast<const h8*>(p);
+        if (kb >= nkb) xv = h8{};
+        b8 hi, lo;
+        split_f16(xv, hi, lo);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) acc[i][j] = mfma_16(wv[j], lo, mfma_16(wv[j], hi, acc[i][j]));
+      }
+    }
+  };
+  constexpr std::integral_constant<int, 0> s0{};
+  constexpr std::integral_constant<int, 1> s1{};
+
+  if (nkb >= 16) {
+    issue_scales(0);
+  } else {   // K < 512: fewer than 16 bytes a row, brought one by one
+    for (int row = tid; row < SROWS; row += NW * 64) {
+      const uint8_t* p = FP && row < TM ? a.xs + (int64_t)x_row<GROUPED>(a, t.m0 + row, t.m_end) * nkb
+                                        : a.ws + ((int64_t)t.e * a.N + min(n0 + row - SOFF, a.N - 1)) * nkb;
+#pragma unroll
+      for (int b = 0; b < 15; ++b) sc[row * 16 + b] = p[min(b, nkb - 1)];
+    }
+  }
+#pragma unroll
+  for (int it = 0; it < RING; ++it)
+    if (it * 4 < nkb) {
+#pragma unroll
+      for (int q = 0; q < QD; ++q) issue(it, smem + it * STAGE, q);
+    }
+  wait_loads<(RING - 1) * QD>();
+  barrier();
+  Frag f0 = read(smem, 0), f1;
+  const int groups = nkb >> 4;
+  uint8_t* cur = smem;   // the place of the stage at hand
+  auto next_place = [&](uint8_t* p) { return p == smem + (RING - 1) * STAGE ? smem : p + STAGE; };
+#pragma unroll 1
+  for (int g = 0; g < groups; ++g) {
+    u4 sa[FP ? MI : 1], sb[NI];   // the group's scale bytes of this lane's rows
+    const uint8_t* sp = sc + (g & 1) * (SROWS * 16) + fr * 16;
+    if constexpr (FP) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) sa[i] = *reinterpret_cast<const u4*>(sp + (wm * MI + i) * 512);
+    }
+#pragma unroll
+    for (int j = 0; j < NI; ++j) sb[j] = *reinterpret_cast<const u4*>(sp + (SOFF + (wn * NI + j) * 32) * 16);
+    if constexpr (XT == F16) {
+      bool fits = true;
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) fits = fits && scale_fits_f16((sb[j][k >> 2] >> (8 * (k & 3))) & 255);
+      if (!__all(fits)) {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {   // the same waits, barriers and loads as below
+          const int it = g * 4 + k;
+          wide_stage(it, cur, sc + (g & 1) * (SROWS * 16), g * 16);
+          wait_loads<(RING - 2) * QD>();
+          barrier();
+#pragma unroll
+          for (int q = 0; q < QD; ++q) issue(it + RING, cur, q);
+          if (k == 0) issue_scales(g + 1);
+          cur = next_place(cur);
+        }
+        f0 = read(cur, 0);
+        continue;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int it = g * 4 + k;
+      Scales w;
+      if constexpr (FP) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) w.a[i] = sa[i][k] >> (8 * h);
+      }
+#pragma unroll
+      for (int j = 0; j < NI; ++j) w.b[j] = sb[j][k] >> (8 * h);
+      f1 = read(cur, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(s0, f0, w, nothing);
+      __builtin_amdgcn_sched_barrier(0);
+      // stage it + 1 has arrived (those after it are on their way), stage it
+      // has been read: its place takes stage it + RING
+      if (k >= 1 && k <= RING - 2) wait_loads<(RING - 2) * QD + 1>();   // the next group's scales are, too
+      else wait_loads<(RING - 2) * QD>();
+      barrier();
+      uint8_t* const nxt = next_place(cur);
+      f0 = read(nxt, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(s1, f1, w, [&](int n) {   // the loads spread over the products: issued at once they hold the wave up
+#pragma unroll
+        for (int q = 0; q < QD; ++q)
+          if (q * (MI * NI) / QD == n) {
+            issue(it + RING, cur, q);
+            __builtin_amdgcn_sched_barrier(FP ? 0 : 2);   // 16 bits: the conversions may pass
+          }
+      });
+      if (k == 0) issue_scales(g + 1);
+      cur = nxt;
+    }
+  }
+  wait_loads<0>();   // nothing is on its way to LDS any more
+  barrier();
+  // The stages of a last group that is not whole (at most four; the ring holds
+  // RING of them, the others are sent for here).
+  for (int it = groups * 4; it * 4 < nkb; ++it) {
+    if (it == groups * 4 + RING) {
+      barrier();     // the places have been read
+#pragma unroll
+      for (int q = 0; q < QD; ++q) issue(it, cur, q);
+      wait_loads<0>();
+      barrier();
+    }
+    // its 16 scale bytes are the row's last ones (K < 512: all); past K: factor 1, zero operands
+    const int k0 = it * 4 + h;
+    auto scale = [&](int row) {
+      const uint8_t* p = sc + (groups & 1) * (SROWS * 16) + (row + fr) * 16 - max(nkb - 16, 0);
+      return (k0 < nkb ? (uint32_t)p[k0] : 127u) | (k0 + 2 < nkb ? (uint32_t)p[k0 + 2] : 127u) << 16;
+    };
+    Scales w;
+    if constexpr (FP) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) w.a[i] = scale((wm * MI + i) * 32);
+    }
+#pragma unroll
+    for (int j = 0; j < NI; ++j) w.b[j] = scale(SOFF + (wn * NI + j) * 32);
+    if constexpr (XT == F16) {
+      bool fits = true;
+#pragma unroll
+      for (int j = 0; j < NI; ++j) fits = fits && scale_fits_f16(w.b[j] & 255) && scale_fits_f16(w.b[j] >> 16);
+      if (!__all(fits)) {
+        wide_stage(it, cur, sc + (groups & 1) * (SROWS * 16), max(nkb - 16, 0));
+        cur = next_place(cur);
+        continue;
+      }
+    }
+    f0 = read(cur, 0);
+    f1 = read(cur, 1);
+    auto clear = [](Frag& f) {
+#pragma unroll
+      for (int j = 0; j < NI; ++j) f.b[j] = u4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int c = 0; c < (FP ? 1 : 4); ++c) f.a[i][c] = u4{0, 0, 0, 0};
+    };
+    if (k0 >= nkb) clear(f0);
+    if (k0 + 2 >= nkb) clear(f1);
+    multiply(s0, f0, w, nothing);
+    multiply(s1, f1, w, nothing);
+    cur = next_place(cur);
+  }
+  store_blocks<MI, NI, GROUPED>(a, t, smem + wave * (32 * (32 * NI + 4) * 4), wm * MI * 32, n0 + wn * NI * 32, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -395,16 +994,110 @@ dim3 ew_grid(int64_t rows, int64_t n8) {
   return dim3((unsigned)std::max<int64_t>(bx, 1), (unsigned)std::min<int64_t>(rows, 65535));
 }
 
+// Which kernel takes a product.  tile 0: mx_rows_kernel with nt column blocks
+// and nw waves a workgroup; 1, 2, 3: mx_tile_kernel on 64 x 64, 128 x 128 and
+// 256 x 256 tiles (16-bit x: 64 x 64, 128 x 128, 128 x 256).  QMX_TILE=0..3 in the environment forces one
+// (tests, tuning).
+struct MxPlan { int tile, nt, nw; int64_t workgroups; };
+
+// The rule is a model of the time in nanoseconds, from what the kernels
+// measured on graph-replayed products of 1..2048 rows with 2048 and 8192
+// columns and K.  A tile's stage of 128 k takes `alone` when its CU runs few
+// tiles (latency) and `shared` for each of the CU's tiles when it runs many:
+//   MXFP4 x   64 x 64: 210, 200   128 x 128: 310, 430   256 x 256: 750, 1200
+//   16-bit x  64 x 64: 400, 360   128 x 128: 800, 1070  128 x 256: 1320, 1840
+// with `start` for the first loads and the stores of each tile in a row on a
+// CU.  The rows kernel takes about 0.75 (16-bit x: 1.05) a block of 16 x 16
+// outputs and chunk of 512 k over the whole chip, after 2500.  For instance 8192 x
+// 8192 weights in bf16: 16 rows 13.0 us (64 x 64 tiles: 26.1), 64 rows 26.1 (rows kernel: 35), 2048 rows 233
+// on 128 x 256 tiles, 273 on 128 x 128, 352 on 64 x 64.  A grouped product's
+// row tiles are estimated: each group's last one half empty.
+MxPlan plan_product(int M, int N, int K, int E, int x_type) {
+  const bool fp = x_type == FP4;
+  MxPlan p = {0, 1, 1, 0};
+  const int64_t chunks = ((int64_t)K + 511) / 512, stages = ((int64_t)K + 127) / 128;
+  const int active = E > 0 ? std::min(E, M) : 1;
+  auto row_tiles = [&](int rows) -> int64_t {
+    if (E == 0) return ((int64_t)M + rows - 1) / rows;
+    return std::max<int64_t>(active, M / rows + active / 2);
+  };
+  if (K > 0) {
+    static const struct { int rows, cols; double alone, shared, start; } tiles[2][3] = {
+        {{64, 64, 400, 360, 2400}, {128, 128, 800, 1070, 3000}, {128, 256, 1320, 1840, 3500}},
+        {{64, 64, 210, 200, 1500}, {128, 128, 310, 430, 2500}, {256, 256, 750, 1200, 3500}}};
+    double best = 2500 + (fp ? 0.75 : 1.05) * (double)(row_tiles(16) * (((int64_t)N + 15) / 16) * chunks);
+    if (row_tiles(16) > 65535) best = 1e300;   // the rows kernel's grid
+    for (int i = 0; i < 3; ++i) {
+      const auto& t = tiles[fp][i];
+      const int64_t n = row_tiles(t.rows) * (((int64_t)N + t.cols - 1) / t.cols), turns = (n + 255) / 256;
+      const double cost = (double)stages * std::max(t.alone, t.shared * (double)turns) + t.start * (1 + 0.25 * (double)(turns - 1));
+      if (cost < best) best = cost, p.tile = i + 1;
+    }
+    const int forced = env_int("QMX_TILE", -1);
+    if (forced >= 0 && forced <= 3) p.tile = forced;
+    if (p.tile) p.workgroups = row_tiles(tiles[fp][p.tile - 1].rows) * (((int64_t)N + tiles[fp][p.tile - 1].cols - 1) / tiles[fp][p.tile - 1].cols);
+  }
+  if (p.tile == 0) {
+    // a wave for every chunk, so that x stays in LDS; where that is more than
+    // fits, and x is read again for every block, two blocks share the reading
+    p.nw = K < 512 ? 1 : chunks <= 2 ? 2 : chunks <= 4 ? 4 : chunks <= 8 ? 8 : 16;
+    const int rows = std::min(M, 16);
+    const int64_t lds = (int64_t)p.nw * 1024 * ((fp ? (rows + 3) / 4 : rows) + 2);
+    if (lds > 160 * 1024) {
+      p.nw = 8;
+      if ((int64_t)N * active >= 16 * 512) p.nt = 2;
+    }
+    p.workgroups = row_tiles(16) * (((int64_t)N + 16 * p.nt - 1) / (16 * p.nt));
+  }
+  return p;
+}
+
 int launch_status() { return hip_status(hipGetLastError()); }
 
-template <int XT, bool GROUPED> void launch_rows(const MxArgs& a, hipStream_t s) {
-  constexpr int NW = 8;
-  const unsigned nb = (unsigned)((a.N + 15) / 16);
-  const int mt = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
-  const unsigned gy = GROUPED ? (unsigned)a.E : (unsigned)((a.M + 16 * mt - 1) / (16 * mt));
-  if (mt == 1) hipLaunchKernelGGL((mx_rows_kernel<XT, 1, NW, GROUPED>), dim3(nb, gy), dim3(NW * 64), 0, s, a);
-  else if (mt == 2) hipLaunchKernelGGL((mx_rows_kernel<XT, 2, NW, GROUPED>), dim3(nb, gy), dim3(NW * 64), 0, s, a);
-  else hipLaunchKernelGGL((mx_rows_kernel<XT, 4, NW, GROUPED>), dim3(nb, gy), dim3(NW * 64), 0, s, a);
+template <int XT, int NT, int NW, bool SHORT, bool GROUPED> int launch_rows(const MxArgs& a, hipStream_t s) {
+  const int64_t gy = GROUPED ? a.E : ((int64_t)a.M + 15) / 16;
+  if (gy > 65535) return QG_E_UNSUPPORTED;
+  const size_t lds = (size_t)NW * rows_x_bytes<XT>(a.M) + 2 * NW * NT * 1024;
+  if constexpr (NW > 4) {
+    if (lds > 160 * 1024) return launch_rows<XT, NT, NW / 2, SHORT, GROUPED>(a, s);
+  }
+  const int64_t blocks = (a.N + 16 * NT - 1) / (16 * NT), active = GROUPED ? std::min(a.E, a.M) : gy;
+  // column blocks a workgroup takes: no more workgroups than keep 32 waves on every CU
+  const int64_t slots = 256 * 32 / NW, share = (blocks * active + slots - 1) / slots;
+  const dim3 grid((unsigned)((blocks + share - 1) / share), (unsigned)gy);
+  if (grid.x == blocks && a.K <= 512 * NW)
+    hipLaunchKernelGGL((mx_rows_kernel<XT, NT, NW, SHORT, false, GROUPED>), grid, dim3(NW * 64), lds, s, a);
+  else
+    hipLaunchKernelGGL((mx_rows_kernel<XT, NT, NW, SHORT, true, GROUPED>), grid, dim3(NW * 64), lds, s, a);
+  return QG_OK;
+}
+
+template <int XT, int MI, int NI, int WM, int WN, int RING, bool GROUPED> int launch_tiles(const MxArgs& a, hipStream_t s) {
+  constexpr int TM = 32 * MI * WM, TN = 32 * NI * WN;
+  const int64_t tn = (a.N + TN - 1) / TN;
+  const int64_t tm = GROUPED ? a.M / TM + std::min(a.E, a.M) : (a.M + TM - 1) / TM;   // at most
+  const int64_t grid = (tn * tm + 7) / 8 * 8;
+  if (grid > INT_MAX) return QG_E_UNSUPPORTED;
+  hipLaunchKernelGGL((mx_tile_kernel<XT, MI, NI, WM, WN, RING, GROUPED>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, s, a, (int)tn);
+  return QG_OK;
+}
+
+template <int XT, bool GROUPED> int launch_product(const MxArgs& a, const MxPlan& p, hipStream_t s) {
+  if constexpr (XT == FP4) {
+    if (p.tile == 3) return launch_tiles<XT, 4, 2, 2, 4, 4, GROUPED>(a, s);
+    if (p.tile == 2) return launch_tiles<XT, 2, 2, 2, 2, 4, GROUPED>(a, s);
+    if (p.tile == 1) return launch_tiles<XT, 1, 1, 2, 2, 4, GROUPED>(a, s);
+  } else {
+    if (p.tile == 3) return launch_tiles<XT, 2, 2, 2, 4, 3, GROUPED>(a, s);
+    if (p.tile == 2) return launch_tiles<XT, 2, 1, 2, 4, 3, GROUPED>(a, s);
+    if (p.tile == 1) return launch_tiles<XT, 1, 1, 2, 2, 3, GROUPED>(a, s);
+  }
+  if (a.K < 512) return launch_rows<XT, 1, 1, true, GROUPED>(a, s);
+  if (p.nt == 2) return launch_rows<XT, 2, 8, false, GROUPED>(a, s);
+  if (p.nw == 2) return launch_rows<XT, 1, 2, false, GROUPED>(a, s);
+  if (p.nw == 4) return launch_rows<XT, 1, 4, false, GROUPED>(a, s);
+  if (p.nw == 8) return launch_rows<XT, 1, 8, false, GROUPED>(a, s);
+  return launch_rows<XT, 1, 16, false, GROUPED>(a, s);
 }
 
 template <bool GROUPED> int run_product(const MxArgs& a, int x_type, void* stream) {
@@ -416,10 +1109,11 @@ template <bool GROUPED> int run_product(const MxArgs& a, int x_type, void* strea
   if (st != QG_OK) return st;
   clear_pending_error();
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (x_type == FP4) launch_rows<FP4, GROUPED>(a, s);
-  else if (x_type == BF16) launch_rows<BF16, GROUPED>(a, s);
-  else launch_rows<F16, GROUPED>(a, s);
-  return launch_status();
+  const MxPlan p = plan_product(a.M, a.N, a.x_rows > 0 ? a.K : 0, GROUPED ? a.E : 0, x_type);
+  if (x_type == FP4) st = launch_product<FP4, GROUPED>(a, p, s);
+  else if (x_type == BF16) st = launch_product<BF16, GROUPED>(a, p, s);
+  else st = launch_product<F16, GROUPED>(a, p, s);
+  return st != QG_OK ? st : launch_status();
 }
 
 // Checks shared by the two products; fills the fields that both use.
@@ -444,7 +1138,6 @@ int setup_product(const void* x, int ldx, int x_type, const uint8_t* xs, int x_r
   a->ldy = ldy; a->y_type = y_type;
   a->rows = nullptr; a->offsets = nullptr; a->row_scale = nullptr; a->E = E;
   a->resid = nullptr; a->ldr = N;
-  a->vec = ldy % 4 == 0;
   return QG_OK;
 }
 
@@ -452,6 +1145,16 @@ int setup_product(const void* x, int ldx, int x_type, const uint8_t* xs, int x_r
 }  // namespace qg
 
 using namespace qg;
+
+extern "C" int qmx_plan(int M, int N, int K, int E, int x_type, int out[4]) {
+  if (M < 0 || N < 0 || K < 0 || E < 0 || K % 32 || (x_type != F16 && x_type != BF16 && x_type != FP4) || !out) return QG_E_ARG;
+  const MxPlan p = plan_product(M, N, K, E, x_type);
+  out[0] = p.tile;
+  out[1] = p.tile ? 0 : p.nt;
+  out[2] = p.tile ? 0 : p.nw;
+  out[3] = (int)std::min<int64_t>(p.workgroups, INT_MAX);
+  return QG_OK;
+}
 
 extern "C" int qmx_quantize(const void* x, int ldx, int x_type, int M, int K, uint8_t* codes, uint8_t* scales,
                             void* stream) {
@@ -517,7 +1220,6 @@ extern "C" int qmx_gemm(const void* x, int ldx, int x_type, const uint8_t* x_sca
     if (!aligned(residual, 16)) return QG_E_ALIGN;
     a.resid = reinterpret_cast<const char*>(residual);
     a.ldr = ldr;
-    a.vec = a.vec && ldr % 4 == 0;
   }
   return run_product<false>(a, x_type, stream);
 }
