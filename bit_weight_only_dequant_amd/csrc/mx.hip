@@ -171,9 +171,14 @@ __device__ __forceinline__ h8 codes_f16(uint32_t c, float sf) {
   return h8{a.x, a.y, b.x, b.y, e.x, e.y, f.x, f.y};
 }
 
-// Scale bytes for which every code times the scale is an exact fp16 number:
-// 0.5 * 2^(104 - 127) = 2^-24, fp16's smallest, and 6 * 2^(140 - 127) = 49152.
-__device__ __forceinline__ bool scale_fits_f16(uint32_t s) { return s - 104u <= 36u; }
+// Scale bytes for which every code times the scale is an exact fp16 number,
+// 104..135: 0.5 * 2^(104 - 127) = 2^-24 is fp16's smallest (141 would be the
+// first too large; 32 in a row are told apart by their upper bits).
+__device__ __forceinline__ bool scale_fits_f16(uint32_t s) { return ((s - 104u) & ~31u) == 0; }
+// not 0 where one of a word's four bytes does not fit (subtraction byte by byte)
+__device__ __forceinline__ uint32_t scales_unfit_f16(uint32_t w) {
+  return (((w | 0x80808080u) - 0x68686868u) ^ (~w & 0x80808080u)) & 0xe0e0e0e0u;
+}
 
 // fp16 x = hi + lo exactly in two bf16 numbers: fp16 has 11 significant bits,
 // hi keeps the upper 8 (truncated), lo the at most 3 left over.  Infinities
@@ -681,6 +686,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
   static_assert(QA * XR * NW == TM && QB * 16 * NW == TN, "rows split evenly over the waves");
   constexpr int SROWS = FP ? TM + TN : TN, SOFF = FP ? TM : 0;   // rows with scales; W's first
   constexpr int STAGE = TM * XB + TN * 64;
+  static_assert(RING >= 3 && RING <= 5, "a group's scales are older than what the last stage before it leaves on its way");
   static_assert(SROWS % 64 == 0 && SROWS / 64 <= NW, "a wave brings the scales of 64 rows");
   static_assert(NW * 32 * (32 * NI + 4) * 4 <= RING * STAGE, "store_blocks' strips");
   // one array: with two, the compiler waits for every direct load before each read
@@ -720,13 +726,18 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
 #pragma unroll
     for (int c = 0; c < 4; ++c) xoff[s][c] = fr * 256 + (((8 * s + 4 * h + c) ^ (fr & 15)) * 16);
   }
-  f16v acc[MI][NI];
+  // a wave of one block keeps two sums of it, so that a product need not wait for the one before
+  constexpr int ACCS = MI * NI == 1 ? 2 : 1;
+  f16v acc[MI][NI], other[1];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j)
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) other[0][k] = 0.f;
+  auto sum = [&](int i, int j, int c) -> f16v& { return ACCS == 2 && (c & 1) ? other[0] : acc[i][j]; };
 
   auto dma = [](const char* from, uint8_t* to) { __builtin_amdgcn_global_load_lds((gptr)from, (lptr)to, 16, 0, 0); };
   auto issue = [&](int it, uint8_t* to, int q) {   // past the end: the rows' last chunk, into a place that is not read any more
@@ -767,7 +778,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
 #pragma unroll
       for (int k = 0; k < MI * NI; ++k) {
         const int i = k / NI, j = k % NI;
-        acc[i][j] = mfma_fp4_32<2 * s>(f.b[j], w.b[j], f.a[i][0], w.a[i], acc[i][j]);
+        sum(i, j, s) = mfma_fp4_32<2 * s>(f.b[j], w.b[j], f.a[i][0], w.a[i], sum(i, j, s));
         between(k);
       }
     } else {
@@ -783,7 +794,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
 #pragma unroll
           for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < NI; ++j) acc[i][j] = mfma_16(wv[j], __builtin_bit_cast(h8, f.a[i][c]), acc[i][j]);
+            for (int j = 0; j < NI; ++j) sum(i, j, c) = mfma_16(wv[j], __builtin_bit_cast(h8, f.a[i][c]), sum(i, j, c));
         } else {
           b8 wv[NI];
 #pragma unroll
@@ -791,7 +802,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
 #pragma unroll
           for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < NI; ++j) acc[i][j] = mfma_16(wv[j], __builtin_bit_cast(b8, f.a[i][c]), acc[i][j]);
+            for (int j = 0; j < NI; ++j) sum(i, j, c) = mfma_16(wv[j], __builtin_bit_cast(b8, f.a[i][c]), sum(i, j, c));
         }
         // between() MI * NI times in all, spread over the four words
 #pragma unroll
@@ -843,7 +854,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
   }
 #pragma unroll
   for (int it = 0; it < RING; ++it)
-    if (it * 4 < nkb) {
+    if (nkb >= 16 || it * 4 < nkb) {   // the waits below count all RING of them
 #pragma unroll
       for (int q = 0; q < QD; ++q) issue(it, smem + it * STAGE, q);
     }
@@ -864,21 +875,21 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
 #pragma unroll
     for (int j = 0; j < NI; ++j) sb[j] = *reinterpret_cast<const u4*>(sp + (SOFF + (wn * NI + j) * 32) * 16);
     if constexpr (XT == F16) {
-      bool fits = true;
+      uint32_t unfit = 0;
 #pragma unroll
       for (int j = 0; j < NI; ++j)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) fits = fits && scale_fits_f16((sb[j][k >> 2] >> (8 * (k & 3))) & 255);
-      if (!__all(fits)) {
+        for (int k = 0; k < 4; ++k) unfit |= scales_unfit_f16(sb[j][k]);
+      if (__any(unfit != 0)) {
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {   // the same waits, barriers and loads as below
           const int it = g * 4 + k;
           wide_stage(it, cur, sc + (g & 1) * (SROWS * 16), g * 16);
           wait_loads<(RING - 2) * QD>();
           barrier();
+          if (k == 0) issue_scales(g + 1);
 #pragma unroll
           for (int q = 0; q < QD; ++q) issue(it + RING, cur, q);
-          if (k == 0) issue_scales(g + 1);
           cur = next_place(cur);
         }
         f0 = read(cur, 0);
@@ -901,9 +912,11 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
       __builtin_amdgcn_sched_barrier(0);
       // stage it + 1 has arrived (those after it are on their way), stage it
       // has been read: its place takes stage it + RING
-      if (k >= 1 && k <= RING - 2) wait_loads<(RING - 2) * QD + 1>();   // the next group's scales are, too
+      // (and in stages 1 and 2 the next group's scales, which are read after stage 3)
+      if (k >= 1 && k <= 2 && k <= RING - 2) wait_loads<(RING - 2) * QD + 1>();
       else wait_loads<(RING - 2) * QD>();
       barrier();
+      if (k == 0) issue_scales(g + 1);
       uint8_t* const nxt = next_place(cur);
       f0 = read(nxt, 0);
       __builtin_amdgcn_sched_barrier(0);
@@ -915,7 +928,6 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
             __builtin_amdgcn_sched_barrier(FP ? 0 : 2);   // 16 bits: the conversions may pass
           }
       });
-      if (k == 0) issue_scales(g + 1);
       cur = nxt;
     }
   }
@@ -970,6 +982,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
     multiply(s1, f1, w, nothing);
     cur = next_place(cur);
   }
+  if constexpr (ACCS == 2) acc[0][0] += other[0];
   store_blocks<MI, NI, GROUPED>(a, t, smem + wave * (32 * (32 * NI + 4) * 4), wm * MI * 32, n0 + wn * NI * 32, acc);
 }
 
@@ -1004,11 +1017,11 @@ struct MxPlan { int tile, nt, nw; int64_t workgroups; };
 // measured on graph-replayed products of 1..2048 rows with 2048 and 8192
 // columns and K.  A tile's stage of 128 k takes `alone` when its CU runs few
 // tiles (latency) and `shared` for each of the CU's tiles when it runs many:
-//   MXFP4 x   64 x 64: 210, 200   128 x 128: 310, 430   256 x 256: 750, 1200
+//   MXFP4 x   64 x 64: 165, 200   128 x 128: 310, 430   256 x 256: 750, 1200
 //   16-bit x  64 x 64: 400, 360   128 x 128: 800, 1070  128 x 256: 1320, 1840
 // with `start` for the first loads and the stores of each tile in a row on a
 // CU.  The rows kernel takes about 0.75 (16-bit x: 1.05) a block of 16 x 16
-// outputs and chunk of 512 k over the whole chip, after 2500.  For instance 8192 x
+// outputs and chunk of 512 k over the whole chip, after 2300.  For instance 8192 x
 // 8192 weights in bf16: 16 rows 13.0 us (64 x 64 tiles: 26.1), 64 rows 26.1 (rows kernel: 35), 2048 rows 233
 // on 128 x 256 tiles, 273 on 128 x 128, 352 on 64 x 64.  A grouped product's
 // row tiles are estimated: each group's last one half empty.
@@ -1024,8 +1037,8 @@ MxPlan plan_product(int M, int N, int K, int E, int x_type) {
   if (K > 0) {
     static const struct { int rows, cols; double alone, shared, start; } tiles[2][3] = {
         {{64, 64, 400, 360, 2400}, {128, 128, 800, 1070, 3000}, {128, 256, 1320, 1840, 3500}},
-        {{64, 64, 210, 200, 1500}, {128, 128, 310, 430, 2500}, {256, 256, 750, 1200, 3500}}};
-    double best = 2500 + (fp ? 0.75 : 1.05) * (double)(row_tiles(16) * (((int64_t)N + 15) / 16) * chunks);
+        {{64, 64, 165, 200, 2300}, {128, 128, 310, 430, 2500}, {256, 256, 750, 1200, 3500}}};
+    double best = 2300 + (fp ? 0.75 : 1.05) * (double)(row_tiles(16) * (((int64_t)N + 15) / 16) * chunks);
     if (row_tiles(16) > 65535) best = 1e300;   // the rows kernel's grid
     for (int i = 0; i < 3; ++i) {
       const auto& t = tiles[fp][i];
