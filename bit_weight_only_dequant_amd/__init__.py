@@ -450,119 +450,130 @@ def loop_block_persistent(x, linears: Sequence[QuantLinear], L: int, scratch=Non
 MX_F16, MX_BF16, MX_F32, MX_FP4 = 0, 1, 2, 3
 MX_BLOCK = 32
 _MX_TYPE = {torch.float16: MX_F16, torch.bfloat16: MX_BF16, torch.float32: MX_F32}
+_U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
 
 
-class _MXCall:
-    """What a call on `device` needs around it: the device made current if it
-    is not, and the stream (outputs are allocated under a stream that is named,
-    so their memory is not reused from work still pending on another)."""
-
-    def __init__(self, device, stream):
-        self._device, self._given = device, stream
-        self._ctx = None
-
-    def __enter__(self):
-        if self._given is not None:
-            if self._given.device != self._device:
-                raise ValueError(f"stream is on {self._given.device}, the tensors on {self._device}")
-            self._ctx = torch.cuda.stream(self._given)
-            self._ctx.__enter__()
-            return self._given.cuda_stream
-        if self._device.index != torch.cuda.current_device():
-            self._ctx = torch.cuda.device(self._device)
-            self._ctx.__enter__()
-        return torch.cuda.current_stream(self._device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+def _mx_elsewhere(x, stream):
+    """The context that a call on x needs when it may not simply run on the
+    current stream (None if it may): another stream is made current, so that
+    what the call allocates belongs to it, or x's device is."""
+    if not x.is_cuda:
+        raise ValueError("the tensors must be on the GPU")
+    if stream is not None:
+        if stream.device != x.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+        return torch.cuda.stream(stream)
+    if x.get_device() != torch._C._cuda_getDevice():
+        return torch.cuda.device(x.device)
+    return None
 
 
-def _mx_float(t, what, types=_MX_TYPE):
+def _mx_stream(dev: int) -> int:
+    """The current stream of the current device (the handle alone: these calls
+    take microseconds, and so does making a stream object)."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _mx_float(t, what, dev, shape=None, types=_MX_TYPE):
     """A 2-d floating tensor with unit column stride -> (its type, its row stride)."""
-    _dev(t, what)
-    if t.dtype not in types or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what} must be a 2-d tensor of {', '.join(str(d) for d in types)} with unit column stride")
-    return _MX_TYPE[t.dtype], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    xt, sh = types.get(t.dtype), t.shape
+    if xt is None or len(sh) != 2 or t.get_device() != dev or (shape is not None and sh != shape):
+        raise ValueError(f"{what} must be {list(shape) if shape else 'a matrix'} of "
+                         f"{' or '.join(str(d) for d in types)} on GPU {dev}; got {t.dtype} {list(sh)} on {t.device}")
+    row, col = t.stride()
+    if col != 1 and sh[1] > 1:
+        raise ValueError(f"{what} must have unit column stride")
+    return xt, row if sh[0] > 1 else sh[1]
 
 
-def _mx_bytes(t, shape, what, device):
-    """A contiguous uint8 tensor of this shape on this device."""
-    if t.dtype != torch.uint8 or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous uint8 tensor of shape {shape} on {device}")
+def _mx_matrix(codes, scales, what, dev, dims=2):
+    """The shape of a codes tensor [.., R, K/2] that its scales [.., R, K/32] fit."""
+    sh = codes.shape
+    if (codes.dtype is _U8 and scales.dtype is _U8 and len(sh) == dims and sh[-1] % 16 == 0
+            and scales.shape == (*sh[:-1], sh[-1] // 16) and codes.get_device() == dev and scales.get_device() == dev
+            and codes.is_contiguous() and scales.is_contiguous()):
+        return sh
+    raise ValueError(f"{what} must be contiguous uint8 codes [{'.., ' * (dims - 2)}R, K/2] and scales of as many rows and "
+                     f"K/32 columns, K a multiple of {MX_BLOCK}, on GPU {dev}; got {codes.dtype} {list(sh)} on "
+                     f"{codes.device} and {scales.dtype} {list(scales.shape)} on {scales.device}")
 
 
-def _mx_vector(t, dtype, n, what, device):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements on {device}")
+def _mx_vector(t, dtype, n, what, dev):
+    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of {n} elements on GPU {dev}")
+    return t.data_ptr()
 
 
 def mx_quantize(x, codes=None, scales=None, stream=None):
     """x [M, K] (fp16, bf16 or fp32, K a multiple of 32, unit column stride) ->
     (codes [M, K/2], scales [M, K/32]) in MXFP4; see qmx_quantize."""
-    xt, ldx = _mx_float(x, "x")
+    ctx = _mx_elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return mx_quantize(x, codes, scales)
+    dev = x.get_device()
+    xt, ldx = _mx_float(x, "x", dev)
     M, K = x.shape
     if K % MX_BLOCK:
         raise ValueError(f"K = {K} is not a multiple of {MX_BLOCK}")
-    with _MXCall(x.device, stream) as s:
-        if codes is None:
-            codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
-        else:
-            _mx_bytes(codes, (M, K // 2), "codes", x.device)
-        if scales is None:
-            scales = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
-        else:
-            _mx_bytes(scales, (M, K // 32), "scales", x.device)
-        _check(_lib.qmx_quantize(x.data_ptr(), ldx, xt, M, K, codes.data_ptr(), scales.data_ptr(), s), "qmx_quantize")
+    if codes is None:
+        codes = x.new_empty((M, K // 2), dtype=_U8)
+    if scales is None:
+        scales = x.new_empty((M, K // 32), dtype=_U8)
+    if _mx_matrix(codes, scales, "codes and scales", dev) != (M, K // 2):
+        raise ValueError(f"codes must be [{M}, {K // 2}]")
+    st = _lib.qmx_quantize(x.data_ptr(), ldx, xt, M, K, codes.data_ptr(), scales.data_ptr(), _mx_stream(dev))
+    if st:
+        raise QGemmError(st, "qmx_quantize")
     return codes, scales
 
 
 def mx_dequantize(codes, scales, dtype=torch.float16, out=None, stream=None):
     """The values of an MXFP4 matrix as [M, K] of `dtype` (fp16, bf16 or fp32),
     or into `out` (whose type counts then); see qmx_dequantize."""
-    _dev(codes, "codes"); _dev(scales, "scales")
-    if codes.dim() != 2 or codes.shape[1] % 16:
-        raise ValueError("codes must be uint8 [M, K/2], K a multiple of 32")
-    M, K = codes.shape[0], codes.shape[1] * 2
-    _mx_bytes(codes, (M, K // 2), "codes", codes.device)
-    _mx_bytes(scales, (M, K // 32), "scales", codes.device)
-    if out is None and dtype not in _MX_TYPE:
-        raise ValueError(f"dtype must be one of {', '.join(str(d) for d in _MX_TYPE)}")
-    with _MXCall(codes.device, stream) as s:
-        if out is None:
-            out = torch.empty((M, K), dtype=dtype, device=codes.device)
-        yt, ldy = _mx_float(out, "out")
-        if tuple(out.shape) != (M, K) or out.device != codes.device:
-            raise ValueError(f"out must be [{M}, {K}] on {codes.device}")
-        _check(_lib.qmx_dequantize(codes.data_ptr(), scales.data_ptr(), M, K, out.data_ptr(), ldy, yt, s),
-               "qmx_dequantize")
+    ctx = _mx_elsewhere(codes, stream)
+    if ctx is not None:
+        with ctx:
+            return mx_dequantize(codes, scales, dtype, out)
+    dev = codes.get_device()
+    M, half = _mx_matrix(codes, scales, "codes and scales", dev)
+    if out is None:
+        if dtype not in _MX_TYPE:
+            raise ValueError(f"dtype must be one of {', '.join(str(d) for d in _MX_TYPE)}")
+        out = codes.new_empty((M, 2 * half), dtype=dtype)
+    yt, ldy = _mx_float(out, "out", dev, (M, 2 * half))
+    st = _lib.qmx_dequantize(codes.data_ptr(), scales.data_ptr(), M, 2 * half, out.data_ptr(), ldy, yt, _mx_stream(dev))
+    if st:
+        raise QGemmError(st, "qmx_dequantize")
     return out
 
 
-def _mx_x(x, x_scales, K):
+_MX_X16 = {torch.float16: MX_F16, torch.bfloat16: MX_BF16}
+
+
+def _mx_x(x, x_scales, K, dev):
     """(type, leading dimension, scales pointer) of a product's left operand."""
     if x_scales is None:
-        xt, ldx = _mx_float(x, "x", (torch.float16, torch.bfloat16))
+        xt, ldx = _mx_float(x, "x (without x_scales)", dev, None, _MX_X16)
         if x.shape[1] != K:
             raise ValueError(f"x must have {K} columns, as w has; got {x.shape[1]}")
         return xt, ldx, None
-    _dev(x, "x"); _dev(x_scales, "x_scales")
-    if x.dim() != 2:
-        raise ValueError("x must be 2-d")
-    _mx_bytes(x, (x.shape[0], K // 2), "x (codes)", x.device)
-    _mx_bytes(x_scales, (x.shape[0], K // 32), "x_scales", x.device)
+    if _mx_matrix(x, x_scales, "x and x_scales", dev)[1] != K // 2:
+        raise ValueError(f"x (codes) must have {K // 2} columns, as w has; got {x.shape[1]}")
     return MX_FP4, K, x_scales.data_ptr()
 
 
-def _mx_y(out, M, N, out_dtype, device):
+def _mx_y(x, x_scales, out, out_dtype, M, N, dev):
     """(out, its type, its leading dimension)."""
     if out is None:
-        if out_dtype not in _MX_TYPE:
+        if out_dtype is None:
+            out_dtype = x.dtype if x_scales is None else torch.float16
+        elif out_dtype not in _MX_TYPE:
             raise ValueError(f"out_dtype must be one of {', '.join(str(d) for d in _MX_TYPE)}")
-        return torch.empty((M, N), dtype=out_dtype, device=device), _MX_TYPE[out_dtype], N
-    yt, ldy = _mx_float(out, "out")
-    if tuple(out.shape) != (M, N) or out.device != device or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError(f"out must be [{M}, {N}] of {out_dtype or out.dtype} on {device}")
+        return x.new_empty((M, N), dtype=out_dtype), _MX_TYPE[out_dtype], N
+    yt, ldy = _mx_float(out, "out", dev, (M, N))
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
     return out, yt, ldy
 
 
@@ -571,26 +582,24 @@ def mx_gemm(x, w, w_scales, x_scales=None, out=None, out_dtype=None, residual=No
     x: fp16 or bf16 [M, K] with unit column stride, or MXFP4 codes with
     x_scales.  y: out_dtype (fp16, bf16 or fp32; x's type by default, fp16 for
     MXFP4 x); see qmx_gemm."""
-    _dev(w, "w"); _dev(w_scales, "w_scales")
-    if w.dim() != 2 or w.shape[1] % 16:
-        raise ValueError("w must be uint8 [N, K/2], K a multiple of 32")
-    N, K = w.shape[0], w.shape[1] * 2
-    xt, ldx, xs = _mx_x(x, x_scales, K)
-    device, M = x.device, x.shape[0]
-    _mx_bytes(w, (N, K // 2), "w", device)
-    _mx_bytes(w_scales, (N, K // 32), "w_scales", device)
-    if out is None and out_dtype is None:
-        out_dtype = x.dtype if x_scales is None else torch.float16
-    with _MXCall(device, stream) as s:
-        y, yt, ldy = _mx_y(out, M, N, out_dtype, device)
-        rp, ldr = None, N
-        if residual is not None:
-            rt, ldr = _mx_float(residual, "residual")
-            if rt != yt or tuple(residual.shape) != (M, N) or residual.device != device:
-                raise ValueError(f"residual must be [{M}, {N}] of {y.dtype} on {device}")
-            rp = residual.data_ptr()
-        _check(_lib.qmx_gemm(x.data_ptr(), ldx, xt, xs, w.data_ptr(), w_scales.data_ptr(), rp, ldr, M, N, K,
-                             y.data_ptr(), ldy, yt, s), "qmx_gemm")
+    ctx = _mx_elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return mx_gemm(x, w, w_scales, x_scales, out, out_dtype, residual)
+    dev = x.get_device()
+    N, half = _mx_matrix(w, w_scales, "w and w_scales", dev)
+    K = 2 * half
+    xt, ldx, xs = _mx_x(x, x_scales, K, dev)
+    M = x.shape[0]
+    y, yt, ldy = _mx_y(x, x_scales, out, out_dtype, M, N, dev)
+    rp, ldr = None, N
+    if residual is not None:
+        _, ldr = _mx_float(residual, "residual", dev, (M, N), {y.dtype: yt})
+        rp = residual.data_ptr()
+    st = _lib.qmx_gemm(x.data_ptr(), ldx, xt, xs, w.data_ptr(), w_scales.data_ptr(), rp, ldr, M, N, K, y.data_ptr(),
+                       ldy, yt, _mx_stream(dev))
+    if st:
+        raise QGemmError(st, "qmx_gemm")
     return y
 
 
@@ -604,28 +613,27 @@ def mx_gemm_grouped(x, w, w_scales, offsets, x_scales=None, rows=None, row_scale
     rows, or the number of rows of x.  Rows of `out` that no group covers are
     left as they were (a fresh result holds unset values there); see
     qmx_gemm_grouped."""
-    _dev(w, "w"); _dev(w_scales, "w_scales"); _dev(offsets, "offsets"); _dev(rows, "rows"); _dev(row_scale, "row_scale")
-    if w.dim() != 3 or w.shape[2] % 16:
-        raise ValueError("w must be uint8 [E, N, K/2], K a multiple of 32")
-    E, N, K = w.shape[0], w.shape[1], w.shape[2] * 2
-    xt, ldx, xs = _mx_x(x, x_scales, K)
-    device, xr = x.device, x.shape[0]
-    _mx_bytes(w, (E, N, K // 2), "w", device)
-    _mx_bytes(w_scales, (E, N, K // 32), "w_scales", device)
-    _mx_vector(offsets, torch.int32, E + 1, "offsets", device)
-    T = xr
+    ctx = _mx_elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return mx_gemm_grouped(x, w, w_scales, offsets, x_scales, rows, row_scale, out, out_dtype)
+    dev = x.get_device()
+    E, N, half = _mx_matrix(w, w_scales, "w and w_scales", dev, 3)
+    K = 2 * half
+    xt, ldx, xs = _mx_x(x, x_scales, K, dev)
+    T = x.shape[0]
+    op = _mx_vector(offsets, _I32, E + 1, "offsets", dev)
+    rp = sp = None
     if rows is not None:
-        T = rows.shape[0] if rows.dim() == 1 else -1
-        _mx_vector(rows, torch.int32, T, "rows", device)
+        T = rows.numel()
+        rp = _mx_vector(rows, _I32, T, "rows", dev)
     if row_scale is not None:
-        _mx_vector(row_scale, torch.float32, T, "row_scale", device)
-    if out is None and out_dtype is None:
-        out_dtype = x.dtype if x_scales is None else torch.float16
-    with _MXCall(device, stream) as s:
-        y, yt, ldy = _mx_y(out, T, N, out_dtype, device)
-        _check(_lib.qmx_gemm_grouped(x.data_ptr(), ldx, xt, xs, xr, _ptr(rows), w.data_ptr(), w_scales.data_ptr(),
-                                     offsets.data_ptr(), E, T, _ptr(row_scale), N, K, y.data_ptr(), ldy, yt, s),
-               "qmx_gemm_grouped")
+        sp = _mx_vector(row_scale, _F32, T, "row_scale", dev)
+    y, yt, ldy = _mx_y(x, x_scales, out, out_dtype, T, N, dev)
+    st = _lib.qmx_gemm_grouped(x.data_ptr(), ldx, xt, xs, x.shape[0], rp, w.data_ptr(), w_scales.data_ptr(), op, E, T, sp,
+                               N, K, y.data_ptr(), ldy, yt, _mx_stream(dev))
+    if st:
+        raise QGemmError(st, "qmx_gemm_grouped")
     return y
 
 
@@ -641,12 +649,9 @@ class MXLinear:
     of QuantLinear."""
 
     def __init__(self, codes, scales):
-        _dev(codes, "codes"); _dev(scales, "scales")
-        if codes.dim() != 2 or codes.shape[1] % 16:
-            raise ValueError("codes must be uint8 [N, K/2], K a multiple of 32")
-        self.N, self.K = codes.shape[0], codes.shape[1] * 2
-        _mx_bytes(codes, (self.N, self.K // 2), "codes", codes.device)
-        _mx_bytes(scales, (self.N, self.K // 32), "scales", codes.device)
+        _dev(codes, "codes")
+        self.N, half = _mx_matrix(codes, scales, "codes and scales", codes.get_device())
+        self.K = 2 * half
         self.codes, self.scales = codes, scales
         self.weight_bytes = codes.numel() + scales.numel()
 

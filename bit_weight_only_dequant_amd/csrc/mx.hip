@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <type_traits>
 
@@ -1067,6 +1068,17 @@ MxPlan plan_product(int M, int N, int K, int E, int x_type) {
 
 int launch_status() { return hip_status(hipGetLastError()); }
 
+// QG_OK when there is a device to launch on.  Asking takes the runtime about a
+// microsecond; once one was there it is not asked again.
+int device_present() {
+  static std::atomic<bool> seen{false};
+  if (seen.load(std::memory_order_relaxed)) return QG_OK;
+  int dev = 0;
+  const int st = current_device(&dev);
+  if (st == QG_OK) seen.store(true, std::memory_order_relaxed);
+  return st;
+}
+
 template <int XT, int NT, int NW, bool SHORT, bool GROUPED> int launch_rows(const MxArgs& a, hipStream_t s) {
   const int64_t gy = GROUPED ? a.E : ((int64_t)a.M + 15) / 16;
   if (gy > 65535) return QG_E_UNSUPPORTED;
@@ -1114,8 +1126,7 @@ template <int XT, bool GROUPED> int launch_product(const MxArgs& a, const MxPlan
 }
 
 template <bool GROUPED> int run_product(const MxArgs& a, int x_type, void* stream) {
-  int dev = 0;
-  int st = current_device(&dev);
+  int st = device_present();
   if (st != QG_OK) return st;
   const void* ptrs[9] = {a.x, a.xs, a.w, a.ws, a.rows, a.offsets, a.row_scale, a.resid, a.y};
   st = check_device_pointers(ptrs, 9);
@@ -1174,8 +1185,7 @@ extern "C" int qmx_quantize(const void* x, int ldx, int x_type, int M, int K, ui
   int st = check_matrix(x, ldx, x_type, M, K, codes, scales);
   if (st != QG_OK) return st;
   if (M == 0 || K == 0) return QG_OK;
-  int dev = 0;
-  st = current_device(&dev);
+  st = device_present();
   if (st != QG_OK) return st;
   const void* ptrs[3] = {x, codes, scales};
   st = check_device_pointers(ptrs, 3);
@@ -1200,8 +1210,7 @@ extern "C" int qmx_dequantize(const uint8_t* codes, const uint8_t* scales, int M
   int st = check_matrix(y, ldy, y_type, M, K, codes, scales);
   if (st != QG_OK) return st;
   if (M == 0 || K == 0) return QG_OK;
-  int dev = 0;
-  st = current_device(&dev);
+  st = device_present();
   if (st != QG_OK) return st;
   const void* ptrs[3] = {codes, scales, y};
   st = check_device_pointers(ptrs, 3);
