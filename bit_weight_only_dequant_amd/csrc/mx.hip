@@ -238,46 +238,38 @@ template <int C, typename E> __device__ __forceinline__ void put(E* p, const E (
   }
 }
 
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(f16 v) { return (float)v; }
+__device__ __forceinline__ float to_f32(bf16 v) { return bits_f32((uint32_t)__builtin_bit_cast(uint16_t, v) << 16); }
+
 // C (4 or 8) consecutive outputs of one row, columns n .. n+C-1 of row m: the
 // factor and the residual in fp32, one rounding.  Rows of any pitch are stored
 // in one piece (the device takes vector accesses at element alignment).
-template <int C> __device__ __forceinline__ void store_cols(const MxArgs& a, int m, int n, float (&v)[C], float rs) {
-  const int64_t o = (int64_t)m * a.ldy + n, ro = (int64_t)m * a.ldr + n;
+template <int YT, int C> __device__ __forceinline__ void store_cols_as(const MxArgs& a, int m, int n, float (&v)[C], float factor) {
+  typedef typename Elem<YT>::type E;
   const bool whole = n + C <= a.N;
   const int have = min(a.N - n, C);
 #pragma unroll
-  for (int i = 0; i < C; ++i) v[i] *= rs;
-  if (a.y_type == F32) {
-    if (a.resid) {
-      float r[C] = {};
-      const float* rp = reinterpret_cast<const float*>(a.resid) + ro;
-      if (whole) get(rp, r);
-      else for (int i = 0; i < C; ++i) if (i < have) r[i] = rp[i];
-#pragma unroll
-      for (int i = 0; i < C; ++i) v[i] += r[i];
-    }
-    float* y = reinterpret_cast<float*>(a.y) + o;
-    if (whole) put(y, v);
-    else for (int i = 0; i < C; ++i) if (i < have) y[i] = v[i];
-    return;
-  }
-  const bool half = a.y_type == F16;
+  for (int i = 0; i < C; ++i) v[i] *= factor;
   if (a.resid) {
-    uint16_t r[C] = {};
-    const uint16_t* rp = reinterpret_cast<const uint16_t*>(a.resid) + ro;
+    E r[C] = {};
+    const E* rp = reinterpret_cast<const E*>(a.resid) + (int64_t)m * a.ldr + n;
     if (whole) get(rp, r);
     else for (int i = 0; i < C; ++i) if (i < have) r[i] = rp[i];
 #pragma unroll
-    for (int i = 0; i < C; ++i)
-      v[i] += half ? (float)__builtin_bit_cast(f16, r[i]) : bits_f32((uint32_t)r[i] << 16);
+    for (int i = 0; i < C; ++i) v[i] += to_f32(r[i]);
   }
-  uint16_t q[C];
+  E q[C];
 #pragma unroll
-  for (int i = 0; i < C; ++i)
-    q[i] = half ? __builtin_bit_cast(uint16_t, (f16)v[i]) : __builtin_bit_cast(uint16_t, (bf16)v[i]);
-  uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + o;
+  for (int i = 0; i < C; ++i) q[i] = (E)v[i];
+  E* y = reinterpret_cast<E*>(a.y) + (int64_t)m * a.ldy + n;
   if (whole) put(y, q);
   else for (int i = 0; i < C; ++i) if (i < have) y[i] = q[i];
+}
+template <int C> __device__ __forceinline__ void store_cols(const MxArgs& a, int m, int n, float (&v)[C], float factor) {
+  if (a.y_type == F32) store_cols_as<F32, C>(a, m, n, v, factor);
+  else if (a.y_type == F16) store_cols_as<F16, C>(a, m, n, v, factor);
+  else store_cols_as<BF16, C>(a, m, n, v, factor);
 }
 
 // A grouped product's slots of expert e, kept within [0, T] whatever the
@@ -557,21 +549,33 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
 // the offsets: lane by lane the tiles of 64 groups, a running sum, a vote.
 struct Tile { int e, m0, m_end, tn; };
 
+// the sum of v over the lanes up to and with this one
+__device__ __forceinline__ int wave_running_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);    // row_shr:1, then 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row 0's sum to row 1, row 2's to row 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // the first two rows' to the others
+  return v;
+}
+
 template <int TM, bool GROUPED>
 __device__ __forceinline__ bool find_tile(const MxArgs& a, int tiles_n, Tile& t) {
-  int tiles_m = 0;
+  int tiles_m = 0, b = 0, e = 0, n = 0, sum = 0;
   const int lane = threadIdx.x & 63;
+  auto scan = [&](int e0) {   // this lane's group: its rows b .. e, its tiles n, the tiles up to and with it
+    n = b = e = 0;
+    if (e0 + lane < a.E) {
+      group_bounds(a, e0 + lane, b, e);
+      n = (e - b + TM - 1) / TM;
+    }
+    sum = wave_running_sum(n);
+  };
   if constexpr (GROUPED) {
     for (int e0 = 0; e0 < a.E; e0 += 64) {
-      int n = 0;
-      if (e0 + lane < a.E) {
-        int b, e;
-        group_bounds(a, e0 + lane, b, e);
-        n = (e - b + TM - 1) / TM;
-      }
-#pragma unroll
-      for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d);
-      tiles_m += n;
+      scan(e0);
+      tiles_m += __builtin_amdgcn_readlane(sum, 63);
     }
   } else {
     tiles_m = (a.M + TM - 1) / TM;
@@ -589,26 +593,17 @@ __device__ __forceinline__ bool find_tile(const MxArgs& a, int tiles_n, Tile& t)
   t.e = 0;
   if constexpr (GROUPED) {
     for (int e0 = 0; e0 < a.E; e0 += 64) {
-      int n = 0, b = 0, e = 0;
-      if (e0 + lane < a.E) {
-        group_bounds(a, e0 + lane, b, e);
-        n = (e - b + TM - 1) / TM;
-      }
-      int sum = n;   // tiles of the groups up to and with this lane's
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(sum, d);
-        if (lane >= d) sum += v;
-      }
+      if (a.E > 64) scan(e0);
       const uint64_t vote = __ballot(sum > tm);
       if (vote) {
         const int who = __builtin_ctzll(vote);
+        const int end = __builtin_amdgcn_readlane(e, who);
         t.e = e0 + who;
-        t.m0 = __shfl(b, who) + (tm - __shfl(sum - n, who)) * TM;
-        t.m_end = min(__shfl(e, who), t.m0 + TM);
-        return true;
+        t.m0 = __builtin_amdgcn_readlane(b, who) + (tm - __builtin_amdgcn_readlane(sum - n, who)) * TM;
+        t.m_end = min(end, t.m0 + TM);
+        return t.m0 >= 0 && t.m0 < t.m_end;
       }
-      tm -= __shfl(sum, 63);
+      tm -= __builtin_amdgcn_readlane(sum, 63);
     }
     return false;
   }
@@ -617,19 +612,17 @@ __device__ __forceinline__ bool find_tile(const MxArgs& a, int tiles_n, Tile& t)
   return true;
 }
 
-
 // Stores a wave's MI x NI blocks of 32 x 32 (element 4 q + k of lane 32 h + r:
 // column 8 q + 4 h + k, row r) at rows row0 of the tile and column n0.  Each
 // strip of 32 rows passes through LDS (the wave's own `strip`, rows padded by
 // 16 bytes), so that a lane stores 8 consecutive outputs and 4 NI lanes a
-// contiguous row piece.
-template <int MI, int NI, bool GROUPED>
-__device__ __forceinline__ void store_blocks(const MxArgs& a, const Tile& t, uint8_t* strip, int row0, int n0,
-                                             const f16v (&acc)[MI][NI]) {
+// contiguous row piece.  `info`: a row's factor and whether it has a row of x.
+template <int YT, int MI, int NI, bool GROUPED>
+__device__ __forceinline__ void store_blocks_as(const MxArgs& a, const Tile& t, uint8_t* strip, int row0, int n0,
+                                                const f2* info, const f16v (&acc)[MI][NI]) {
   constexpr int PITCH = 32 * NI + 4, LANES = 4 * NI, ROWS = 64 / LANES;
   const int lane = threadIdx.x & 63;
   float* s = reinterpret_cast<float*>(strip);
-  __syncthreads();                                   // every wave has read its last stage
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
 #pragma unroll
@@ -642,22 +635,34 @@ __device__ __forceinline__ void store_blocks(const MxArgs& a, const Tile& t, uin
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     const int n = n0 + (lane % LANES) * 8;
-#pragma unroll 1
-    for (int r = lane / LANES; r < 32; r += ROWS) {
-      const int m = t.m0 + row0 + i * 32 + r;
-      if (m >= t.m_end || n >= a.N) continue;
-      float v[8];
-      __builtin_memcpy(v, s + r * PITCH + (lane % LANES) * 8, sizeof(v));
-      if (!has_row<GROUPED>(a, m)) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = 0.f;
+    for (int p = 0; p < 32 / ROWS; ++p) {
+      const int r = p * ROWS + lane / LANES, row = row0 + i * 32 + r, m = t.m0 + row;
+      if (m >= t.m_end || n >= a.N) continue;
+      float v[8], factor = 1.f;
+      __builtin_memcpy(v, s + r * PITCH + (lane % LANES) * 8, sizeof(v));
+      if constexpr (GROUPED) {
+        const f2 f = info[row];
+        factor = f.x;
+        if (f.y == 0.f) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = 0.f;
+        }
       }
-      store_cols<8>(a, m, n, v, GROUPED && a.row_scale ? a.row_scale[m] : 1.f);
+      store_cols_as<YT, 8>(a, m, n, v, factor);
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
+}
+template <int MI, int NI, bool GROUPED>
+__device__ __forceinline__ void store_blocks(const MxArgs& a, const Tile& t, uint8_t* strip, int row0, int n0,
+                                             const f2* info, const f16v (&acc)[MI][NI]) {
+  __syncthreads();                                   // every wave has read its last stage
+  if (a.y_type == F32) store_blocks_as<F32, MI, NI, GROUPED>(a, t, strip, row0, n0, info, acc);
+  else if (a.y_type == F16) store_blocks_as<F16, MI, NI, GROUPED>(a, t, strip, row0, n0, info, acc);
+  else store_blocks_as<BF16, MI, NI, GROUPED>(a, t, strip, row0, n0, info, acc);
 }
 
 // A 32 x 32 x 16 product of 16-bit operands.
@@ -691,8 +696,9 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
   static_assert(SROWS % 64 == 0 && SROWS / 64 <= NW, "a wave brings the scales of 64 rows");
   static_assert(NW * 32 * (32 * NI + 4) * 4 <= RING * STAGE, "store_blocks' strips");
   // one array: with two, the compiler waits for every direct load before each read
-  __shared__ __align__(1024) uint8_t smem[RING * STAGE + 2 * SROWS * 16];
+  __shared__ __align__(1024) uint8_t smem[RING * STAGE + 2 * SROWS * 16 + (GROUPED ? TM * 8 : 0)];
   uint8_t* const sc = smem + RING * STAGE;   // scales: two groups of four stages, 16 bytes a row
+  f2* const info = reinterpret_cast<f2*>(sc + 2 * SROWS * 16);   // grouped: a row's factor, and 1 where it has a row of x
   Tile t;
   if (!find_tile<TM, GROUPED>(a, tiles_n, t)) return;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -701,6 +707,10 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
   const int n0 = t.tn * TN;
   const int nkb = a.K >> 5;
 
+  if constexpr (GROUPED) {
+    for (int i = tid; i < t.m_end - t.m0; i += NW * 64)
+      info[i] = f2{a.row_scale ? a.row_scale[t.m0 + i] : 1.f, has_row<true>(a, t.m0 + i) ? 1.f : 0.f};
+  }
   // direct loads: lane l brings a 16-byte chunk of row l / 4 of 16 (16-bit x: row l / 16 of 4)
   const char* src[QD];
 #pragma unroll
@@ -741,13 +751,20 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
   auto sum = [&](int i, int j, int c) -> f16v& { return ACCS == 2 && (c & 1) ? other[0] : acc[i][j]; };
 
   auto dma = [](const char* from, uint8_t* to) { __builtin_amdgcn_global_load_lds((gptr)from, (lptr)to, 16, 0, 0); };
-  auto issue = [&](int it, uint8_t* to, int q) {   // past the end: the rows' last chunk, into a place that is not read any more
-    if (FP || q >= QA) {
-      const int off = min(it * 4 + ((lane & 3) ^ (lane >> 4)), nkb - 1) * 16;
-      dma(src[q] + off, to + (q < QA ? (wave * QA + q) * 1024 : TM * XB + (wave * QB + q - QA) * 1024));
-    } else {
-      const int c = ((lane & 15) ^ (lane >> 4)) ^ (4 * ((wave * QA + q) & 3));
-      dma(src[q] + (int64_t)min(it * 16 + c, nkb * 4 - 1) * 16, to + (wave * QA + q) * 1024);
+  // this lane's chunk of a stage, in 16 bytes
+  auto chunk = [&](int q) { return FP || q >= QA ? (lane & 3) ^ (lane >> 4) : (lane & 15) ^ (lane >> 4) ^ (4 * ((wave * QA + q) & 3)); };
+#pragma unroll
+  for (int q = 0; q < QD; ++q) src[q] += chunk(q) * 16;
+  auto place = [&](uint8_t* to, int q) { return to + (q < QA ? (wave * QA + q) * 1024 : TM * XB + (wave * QB + q - QA) * 1024); };
+  const int whole = nkb >> 2;   // stages that lie within K
+  // past those: the last of them again, into a place that is not read any more
+  auto issue = [&](int it, uint8_t* to, int q) { dma(src[q] + (int64_t)min(it, whole - 1) * (q < QA ? XB : 64), place(to, q)); };
+  // the stage that K ends in: pieces past K are a row's last one
+  auto issue_part = [&](uint8_t* to) {
+#pragma unroll
+    for (int q = 0; q < QD; ++q) {
+      const int per = q < QA ? XB / 16 : 4, last = (nkb & 3) * (per / 4) - 1;
+      dma(src[q] + (int64_t)whole * (16 * per) + (min(chunk(q), last) - chunk(q)) * 16, place(to, q));
     }
   };
   auto issue_scales = [&](int group) {   // the row's last 16 bytes at most
@@ -855,7 +872,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
   }
 #pragma unroll
   for (int it = 0; it < RING; ++it)
-    if (nkb >= 16 || it * 4 < nkb) {   // the waits below count all RING of them
+    if (nkb >= 16 || it < whole) {   // the waits below count all RING of them
 #pragma unroll
       for (int q = 0; q < QD; ++q) issue(it, smem + it * STAGE, q);
     }
@@ -934,13 +951,17 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
   }
   wait_loads<0>();   // nothing is on its way to LDS any more
   barrier();
-  // The stages of a last group that is not whole (at most four; the ring holds
-  // RING of them, the others are sent for here).
+  // The stages of a last group that is not whole (at most four; RING of them
+  // are there, but for the one that K ends in: the others are sent for here).
   for (int it = groups * 4; it * 4 < nkb; ++it) {
-    if (it == groups * 4 + RING) {
+    if (it == groups * 4 + RING || it == whole) {
       barrier();     // the places have been read
+      if (it == whole) {
+        issue_part(cur);
+      } else {
 #pragma unroll
-      for (int q = 0; q < QD; ++q) issue(it, cur, q);
+        for (int q = 0; q < QD; ++q) issue(it, cur, q);
+      }
       wait_loads<0>();
       barrier();
     }
@@ -984,7 +1005,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
     cur = next_place(cur);
   }
   if constexpr (ACCS == 2) acc[0][0] += other[0];
-  store_blocks<MI, NI, GROUPED>(a, t, smem + wave * (32 * (32 * NI + 4) * 4), wm * MI * 32, n0 + wn * NI * 32, acc);
+  store_blocks<MI, NI, GROUPED>(a, t, smem + wave * (32 * (32 * NI + 4) * 4), wm * MI * 32, n0 + wn * NI * 32, info, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -1036,19 +1057,19 @@ MxPlan plan_product(int M, int N, int K, int E, int x_type) {
     return std::max<int64_t>(active, M / rows + active / 2);
   };
   if (K > 0) {
-    static const struct { int rows, cols; double alone, shared, start; } tiles[2][3] = {
-        {{64, 64, 400, 360, 2400}, {128, 128, 800, 1070, 3000}, {128, 256, 1320, 1840, 3500}},
-        {{64, 64, 165, 200, 2300}, {128, 128, 310, 430, 2500}, {256, 256, 750, 1200, 3500}}};
+    static const struct { int rows, cols; double alone, shared, start; } tiles[2][4] = {
+        {{64, 64, 400, 360, 2400}, {64, 128, 450, 560, 2600}, {128, 128, 800, 1070, 3000}, {128, 256, 1320, 1840, 3500}},
+        {{64, 64, 165, 200, 2300}, {64, 128, 200, 300, 2400}, {128, 128, 310, 430, 2500}, {256, 256, 750, 1200, 3500}}};
     double best = 2300 + (fp ? 0.75 : 1.05) * (double)(row_tiles(16) * (((int64_t)N + 15) / 16) * chunks);
     if (row_tiles(16) > 65535) best = 1e300;   // the rows kernel's grid
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const auto& t = tiles[fp][i];
       const int64_t n = row_tiles(t.rows) * (((int64_t)N + t.cols - 1) / t.cols), turns = (n + 255) / 256;
       const double cost = (double)stages * std::max(t.alone, t.shared * (double)turns) + t.start * (1 + 0.25 * (double)(turns - 1));
       if (cost < best) best = cost, p.tile = i + 1;
     }
     const int forced = env_int("QMX_TILE", -1);
-    if (forced >= 0 && forced <= 3) p.tile = forced;
+    if (forced >= 0 && forced <= 4) p.tile = forced;
     if (p.tile) p.workgroups = row_tiles(tiles[fp][p.tile - 1].rows) * (((int64_t)N + tiles[fp][p.tile - 1].cols - 1) / tiles[fp][p.tile - 1].cols);
   }
   if (p.tile == 0) {
@@ -1109,12 +1130,14 @@ template <int XT, int MI, int NI, int WM, int WN, int RING, bool GROUPED> int la
 
 template <int XT, bool GROUPED> int launch_product(const MxArgs& a, const MxPlan& p, hipStream_t s) {
   if constexpr (XT == FP4) {
-    if (p.tile == 3) return launch_tiles<XT, 4, 2, 2, 4, 4, GROUPED>(a, s);
-    if (p.tile == 2) return launch_tiles<XT, 2, 2, 2, 2, 4, GROUPED>(a, s);
+    if (p.tile == 4) return launch_tiles<XT, 4, 2, 2, 4, 4, GROUPED>(a, s);
+    if (p.tile == 3) return launch_tiles<XT, 2, 2, 2, 2, 4, GROUPED>(a, s);
+    if (p.tile == 2) return launch_tiles<XT, 1, 2, 2, 2, 4, GROUPED>(a, s);
     if (p.tile == 1) return launch_tiles<XT, 1, 1, 2, 2, 4, GROUPED>(a, s);
   } else {
-    if (p.tile == 3) return launch_tiles<XT, 2, 2, 2, 4, 3, GROUPED>(a, s);
-    if (p.tile == 2) return launch_tiles<XT, 2, 1, 2, 4, 3, GROUPED>(a, s);
+    if (p.tile == 4) return launch_tiles<XT, 2, 2, 2, 4, 3, GROUPED>(a, s);
+    if (p.tile == 3) return launch_tiles<XT, 2, 1, 2, 4, 3, GROUPED>(a, s);
+    if (p.tile == 2) return launch_tiles<XT, 1, 1, 2, 4, 3, GROUPED>(a, s);
     if (p.tile == 1) return launch_tiles<XT, 1, 1, 2, 2, 3, GROUPED>(a, s);
   }
   if (a.K < 512) return launch_rows<XT, 1, 1, true, GROUPED>(a, s);
@@ -1147,6 +1170,7 @@ int setup_product(const void* x, int ldx, int x_type, const uint8_t* xs, int x_r
   if (!float_type(y_type) || M < 0 || N < 0 || K < 0 || x_rows < 0 || K % 32) return QG_E_ARG;
   if ((x_type == FP4) != (xs != nullptr) && K > 0 && x_rows > 0) return QG_E_ARG;
   if (E == 0 || M == 0 || N == 0) return QG_OK;
+  if (M > INT_MAX - 512 || N > INT_MAX - 512) return QG_E_UNSUPPORTED;   // the kernels round them up in 32 bits
   if (!y || ldy < N) return QG_E_ARG;
   if (K > 0) {
     if (!w || !ws || (x_rows > 0 && !x)) return QG_E_ARG;
