@@ -1030,23 +1030,29 @@ dim3 ew_grid(int64_t rows, int64_t n8) {
 }
 
 // Which kernel takes a product.  tile 0: mx_rows_kernel with nt column blocks
-// and nw waves a workgroup; 1, 2, 3: mx_tile_kernel on 64 x 64, 128 x 128 and
-// 256 x 256 tiles (16-bit x: 64 x 64, 128 x 128, 128 x 256).  QMX_TILE=0..3 in the environment forces one
-// (tests, tuning).
+// and nw waves a workgroup; 1..4: mx_tile_kernel on 64 x 64, 64 x 128, 128 x 128
+// and 256 x 256 tiles (16-bit x: 128 x 256).  QMX_TILE=0..4 in the environment
+// forces one (tests, tuning).
 struct MxPlan { int tile, nt, nw; int64_t workgroups; };
 
 // The rule is a model of the time in nanoseconds, from what the kernels
 // measured on graph-replayed products of 1..2048 rows with 2048 and 8192
-// columns and K.  A tile's stage of 128 k takes `alone` when its CU runs few
-// tiles (latency) and `shared` for each of the CU's tiles when it runs many:
-//   MXFP4 x   64 x 64: 165, 200   128 x 128: 310, 430   256 x 256: 750, 1200
-//   16-bit x  64 x 64: 400, 360   128 x 128: 800, 1070  128 x 256: 1320, 1840
-// with `start` for the first loads and the stores of each tile in a row on a
-// CU.  The rows kernel takes about 0.75 (16-bit x: 1.05) a block of 16 x 16
-// outputs and chunk of 512 k over the whole chip, after 2300.  For instance 8192 x
-// 8192 weights in bf16: 16 rows 13.0 us (64 x 64 tiles: 26.1), 64 rows 26.1 (rows kernel: 35), 2048 rows 233
-// on 128 x 256 tiles, 273 on 128 x 128, 352 on 64 x 64.  A grouped product's
-// row tiles are estimated: each group's last one half empty.
+// columns and K, and on products of 32..16384 rows grouped over 8..64 matrices.
+// A tile's stage of 128 k takes `alone` when its CU runs one tile (latency)
+// and `shared` for each of the CU's tiles when the chip is full; `start` is
+// a tile's first loads and stores, of which the share `more` shows again for every
+// further tile of the CU.  The rows kernel takes `item` for a block of 16 x 16
+// outputs and chunk of 512 k, over the whole chip, and a pause between 16 rows
+// of a group and the next.  For instance 8192 x 8192
+// weights and bf16 x: 16 rows 13.3 us (64 x 64 tiles 24.8), 64 rows on 64 x 64
+// tiles 24.9 (rows kernel 42), 512 rows on 128 x 128 66 (64 x 64 88, 128 x 256
+// 88), 2048 rows on 128 x 256 233 (128 x 128 273).  How many row tiles a
+// grouped product has is estimated: each group's last one half empty.
+struct MxTileCost { int rows, cols; double alone, shared, start, more; };
+constexpr MxTileCost MX_TILES[2][4] = {
+    {{64, 64, 385, 345, 3000, 0.3}, {64, 128, 490, 510, 3200, 0.5}, {128, 128, 770, 1030, 3500, 0.5}, {128, 256, 1290, 1730, 4000, 0.8}},
+    {{64, 64, 165, 180, 2900, 0.3}, {64, 128, 215, 255, 3000, 0.8}, {128, 128, 265, 390, 3300, 0.4}, {256, 256, 720, 1130, 5500, 1.0}}};
+
 MxPlan plan_product(int M, int N, int K, int E, int x_type) {
   const bool fp = x_type == FP4;
   MxPlan p = {0, 1, 1, 0};
@@ -1057,20 +1063,22 @@ MxPlan plan_product(int M, int N, int K, int E, int x_type) {
     return std::max<int64_t>(active, M / rows + active / 2);
   };
   if (K > 0) {
-    static const struct { int rows, cols; double alone, shared, start; } tiles[2][4] = {
-        {{64, 64, 400, 360, 2400}, {64, 128, 450, 560, 2600}, {128, 128, 800, 1070, 3000}, {128, 256, 1320, 1840, 3500}},
-        {{64, 64, 165, 200, 2300}, {64, 128, 200, 300, 2400}, {128, 128, 310, 430, 2500}, {256, 256, 750, 1200, 3500}}};
-    double best = 2300 + (fp ? 0.75 : 1.05) * (double)(row_tiles(16) * (((int64_t)N + 15) / 16) * chunks);
+    const double item = E > 0 ? (fp ? 0.5 : 0.8) : (fp ? 0.9 : 1.7);
+    double best = 2300 + item * (double)(row_tiles(16) * (((int64_t)N + 15) / 16) * chunks);
+    // a grouped call's workgroups go through their group's rows 16 at a time; some groups are large
+    if (E > 0) best += 2500 * (double)(M / (8 * active));
     if (row_tiles(16) > 65535) best = 1e300;   // the rows kernel's grid
+    int64_t tiles[4];
     for (int i = 0; i < 4; ++i) {
-      const auto& t = tiles[fp][i];
-      const int64_t n = row_tiles(t.rows) * (((int64_t)N + t.cols - 1) / t.cols), turns = (n + 255) / 256;
-      const double cost = (double)stages * std::max(t.alone, t.shared * (double)turns) + t.start * (1 + 0.25 * (double)(turns - 1));
+      const MxTileCost& c = MX_TILES[fp][i];
+      tiles[i] = row_tiles(c.rows) * (((int64_t)N + c.cols - 1) / c.cols);
+      const double turns = (double)((tiles[i] + 255) / 256);
+      const double cost = (double)stages * std::max(c.alone, c.shared * turns) + c.start * (1 + c.more * (turns - 1));
       if (cost < best) best = cost, p.tile = i + 1;
     }
     const int forced = env_int("QMX_TILE", -1);
     if (forced >= 0 && forced <= 4) p.tile = forced;
-    if (p.tile) p.workgroups = row_tiles(tiles[fp][p.tile - 1].rows) * (((int64_t)N + tiles[fp][p.tile - 1].cols - 1) / tiles[fp][p.tile - 1].cols);
+    if (p.tile) p.workgroups = tiles[p.tile - 1];
   }
   if (p.tile == 0) {
     // a wave for every chunk, so that x stays in LDS; where that is more than
@@ -1137,7 +1145,7 @@ template <int XT, bool GROUPED> int launch_product(const MxArgs& a, const MxPlan
   } else {
     if (p.tile == 4) return launch_tiles<XT, 2, 2, 2, 4, 3, GROUPED>(a, s);
     if (p.tile == 3) return launch_tiles<XT, 2, 1, 2, 4, 3, GROUPED>(a, s);
-    if (p.tile == 2) return launch_tiles<XT, 1, 1, 2, 4, 3, GROUPED>(a, s);
+    if (p.tile == 2) return launch_tiles<XT, 2, 1, 1, 4, 3, GROUPED>(a, s);
     if (p.tile == 1) return launch_tiles<XT, 1, 1, 2, 2, 3, GROUPED>(a, s);
   }
   if (a.K < 512) return launch_rows<XT, 1, 1, true, GROUPED>(a, s);

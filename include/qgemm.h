@@ -394,10 +394,11 @@ int qmx_gemm_grouped(const void* x, int ldx, int x_type, const uint8_t* x_scales
 /* The kernel a product takes (for tracing and tests; no HIP call).  M: the
  * rows of x, or the slots T of a grouped product of E groups (E = 0: not
  * grouped).
- * out[0] = 0 the kernel for few rows, 1..3 the tiled kernel on 64 x 64,
- * 128 x 128 or 256 x 256 (16-bit x: 128 x 256) outputs; out[1], out[2] = column
- * blocks of 16 and waves a workgroup of the former; out[3] = pieces of y (an
- * estimate where grouped).  QMX_TILE=0..3 in the environment forces out[0].
+ * out[0] = 0 the kernel for few rows, 1..4 the tiled kernel on 64 x 64,
+ * 64 x 128, 128 x 128 or 256 x 256 (16-bit x: 128 x 256) outputs; out[1],
+ * out[2] = column blocks of 16 and waves a workgroup of the former; out[3] =
+ * pieces of y (an estimate where grouped).  QMX_TILE=0..4 in the environment
+ * forces out[0].
  * Errors: QG_E_ARG. */
 int qmx_plan(int M, int N, int K, int E, int x_type, int out[4]);
 
