@@ -319,9 +319,12 @@ template <int N> __device__ __forceinline__ void wait_loads() {
 // W is the first operand, so a lane ends with four consecutive outputs of one
 // row.
 
+// All of this wave's LDS reads have arrived (s_waitcnt lgkmcnt(0)).
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }
+
 // A barrier that waits for LDS accesses only: loads stay on their way.
 __device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+  wait_lds();
   asm volatile("" ::: "memory");        // no LDS access moves across the barrier
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -492,7 +495,7 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
         }
       }
       if (!last) {
-        __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): x has been read, its place may be sent for again
+        wait_lds();   // x has been read, its place may be sent for again
         asm volatile("" ::: "memory");
         ++turn;
         return;
@@ -693,7 +696,8 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
   constexpr int SROWS = FP ? TM + TN : TN, SOFF = FP ? TM : 0;   // rows with scales; W's first
   constexpr int STAGE = TM * XB + TN * 64;
   static_assert(RING >= 3 && RING <= 5, "a group's scales are older than what the last stage before it leaves on its way");
-  static_assert(SROWS % 64 == 0 && SROWS / 64 <= NW, "a wave brings the scales of 64 rows");
+  static_assert(SROWS % 64 == 0, "a load brings the scales of 64 rows");
+  constexpr int QS = (SROWS / 64 + NW - 1) / NW;               // such loads a wave and group
   static_assert(NW * 32 * (32 * NI + 4) * 4 <= RING * STAGE, "store_blocks' strips");
   // one array: with two, the compiler waits for every direct load before each read
   __shared__ __align__(1024) uint8_t smem[RING * STAGE + 2 * SROWS * 16 + (GROUPED ? TM * 8 : 0)];
@@ -721,12 +725,12 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
     src[QA + q] = reinterpret_cast<const char*>(a.w) +
                   ((int64_t)t.e * a.N + min(n0 + (wave * QB + q) * 16 + (lane >> 2), a.N - 1)) * (a.K >> 1);
   // scales: the 16 bytes of a group of stages of row l of 64 (waves to spare bring the same rows again)
-  const int swave = wave % (SROWS / 64);
-  const uint8_t* ssrc;
-  {
-    const int r = swave * 64 + lane;
-    ssrc = FP && r < TM ? a.xs + (int64_t)x_row<GROUPED>(a, t.m0 + r, t.m_end) * nkb
-                        : a.ws + ((int64_t)t.e * a.N + min(n0 + r - SOFF, a.N - 1)) * nkb;
+  const uint8_t* ssrc[QS];
+#pragma unroll
+  for (int q = 0; q < QS; ++q) {
+    const int r = (wave * QS + q) % (SROWS / 64) * 64 + lane;
+    ssrc[q] = FP && r < TM ? a.xs + (int64_t)x_row<GROUPED>(a, t.m0 + r, t.m_end) * nkb
+                           : a.ws + ((int64_t)t.e * a.N + min(n0 + r - SOFF, a.N - 1)) * nkb;
   }
   // fragments: lane l reads row l % 32, MXFP4 chunk 2 s + l / 32 of step s, 16-bit chunks 8 s + 4 (l / 32) + 0..3
   const int fr = lane & 31, h = lane >> 5;
@@ -768,7 +772,10 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
     }
   };
   auto issue_scales = [&](int group) {   // the row's last 16 bytes at most
-    dma(reinterpret_cast<const char*>(ssrc) + min(group * 16, nkb - 16), sc + (group & 1) * (SROWS * 16) + swave * 1024);
+#pragma unroll
+    for (int q = 0; q < QS; ++q)
+      dma(reinterpret_cast<const char*>(ssrc[q]) + min(group * 16, nkb - 16),
+          sc + (group & 1) * (SROWS * 16) + (wave * QS + q) % (SROWS / 64) * 1024);
   };
   auto barrier = [] {
     asm volatile("" ::: "memory");   // no LDS access moves across it
@@ -882,9 +889,8 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
   const int groups = nkb >> 4;
   uint8_t* cur = smem;   // the place of the stage at hand
   auto next_place = [&](uint8_t* p) { return p == smem + (RING - 1) * STAGE ? smem : p + STAGE; };
-#pragma unroll 1
-  for (int g = 0; g < groups; ++g) {
-    u4 sa[FP ? MI : 1], sb[NI];   // the group's scale bytes of this lane's rows
+  u4 sa[FP ? MI : 1], sb[NI];   // a group's scale bytes of this lane's rows
+  auto read_scales = [&](int g) {
     const uint8_t* sp = sc + (g & 1) * (SROWS * 16) + fr * 16;
     if constexpr (FP) {
 #pragma unroll
@@ -892,6 +898,10 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
     }
 #pragma unroll
     for (int j = 0; j < NI; ++j) sb[j] = *reinterpret_cast<const u4*>(sp + (SOFF + (wn * NI + j) * 32) * 16);
+  };
+  read_scales(0);
+#pragma unroll 1
+  for (int g = 0; g < groups; ++g) {
     if constexpr (XT == F16) {
       uint32_t unfit = 0;
 #pragma unroll
@@ -911,6 +921,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
           cur = next_place(cur);
         }
         f0 = read(cur, 0);
+        read_scales(g + 1);
         continue;
       }
     }
@@ -924,6 +935,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
       }
 #pragma unroll
       for (int j = 0; j < NI; ++j) w.b[j] = sb[j][k] >> (8 * h);
+      wait_lds();   // the first step's operands are here; later this would wait for the second's too
       f1 = read(cur, 1);
       __builtin_amdgcn_sched_barrier(0);
       multiply(s0, f0, w, nothing);
@@ -931,12 +943,13 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
       // stage it + 1 has arrived (those after it are on their way), stage it
       // has been read: its place takes stage it + RING
       // (and in stages 1 and 2 the next group's scales, which are read after stage 3)
-      if (k >= 1 && k <= 2 && k <= RING - 2) wait_loads<(RING - 2) * QD + 1>();
+      if (k >= 1 && k <= 2 && k <= RING - 2) wait_loads<(RING - 2) * QD + QS>();
       else wait_loads<(RING - 2) * QD>();
       barrier();
       if (k == 0) issue_scales(g + 1);
       uint8_t* const nxt = next_place(cur);
       f0 = read(nxt, 0);
+      if (k == 3) read_scales(g + 1);
       __builtin_amdgcn_sched_barrier(0);
       multiply(s1, f1, w, [&](int n) {   // the loads spread over the products: issued at once they hold the wave up
 #pragma unroll
@@ -1138,7 +1151,7 @@ template <int XT, int MI, int NI, int WM, int WN, int RING, bool GROUPED> int la
 
 template <int XT, bool GROUPED> int launch_product(const MxArgs& a, const MxPlan& p, hipStream_t s) {
   if constexpr (XT == FP4) {
-    if (p.tile == 4) return launch_tiles<XT, 4, 2, 2, 4, 4, GROUPED>(a, s);
+    if (p.tile == 4) return env_int("QMX_W4", 0) ? launch_tiles<XT, 4, 4, 2, 2, 4, GROUPED>(a, s) : launch_tiles<XT, 4, 2, 2, 4, 4, GROUPED>(a, s);
     if (p.tile == 3) return launch_tiles<XT, 2, 2, 2, 2, 4, GROUPED>(a, s);
     if (p.tile == 2) return launch_tiles<XT, 1, 2, 2, 2, 4, GROUPED>(a, s);
     if (p.tile == 1) return launch_tiles<XT, 1, 1, 2, 2, 4, GROUPED>(a, s);
