@@ -2,6 +2,30 @@
 // back, the product y = x . W^T with MXFP4 weights, and that product grouped
 // by expert with ragged sizes.  The format and the entry points are described
 // in include/qgemm.h.
+//
+// Kernels
+//   mx_quantize, mx_dequantize   elementwise, HBM-bound; the device's own fp4
+//                        conversions (round to nearest even, saturating).
+//                        8192 x 8192 bf16 there and back: 60.2 us, 5.05 TB/s
+//                        of 304 MB (a large copy reaches 5.14).
+//   mx_rows              few rows.  W and its scales go from memory straight to
+//                        the matrix instruction's registers in their stored
+//                        order, x through LDS; waves split K.  1 x 6144 x 2048
+//                        with fp16 x 5.1 us, 8 x 2048 x 8192 with bf16 x 7 us,
+//                        1 x 8192 x 8192 9.9 us (3.6 TB/s), each in a replayed graph.
+//   mx_tile              more rows.  x and W through a ring of LDS stages by
+//                        direct loads.  MXFP4 x: 4096 x 8192 x 8192 146 us (3.8
+//                        PFLOP/s); bf16 x: 2048 x 8192 x 8192 228 us (1.2
+//                        PFLOP/s; the library's bf16 product reaches 1.37).
+// The stored form needs no packing step: 16 consecutive bytes of a row are one
+// block of 32, which is what one lane supplies to v_mfma_scale_f32_16x16x128 and
+// 32x32x64 (fp4 operands, one scale byte a lane), so the products read
+// checkpoints' own layout.
+// Precision.  MXFP4 values meet 16-bit x exactly: code times scale is an exact
+// bf16 number, so bf16 x uses bf16 matrix instructions and loses nothing; with
+// fp16 x it is an exact fp16 number for scales of 2^-23 .. 2^8, and where a wave
+// meets others it multiplies bf16 weights with x split in two exact bf16 parts.
+// Sums are fp32; the one rounding is at the store.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -542,7 +566,7 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// many rows, both sides MXFP4
+// more rows
 // ---------------------------------------------------------------------------
 // Where a workgroup's tile lies: group e, rows m0 .. m_end of y (at most TM of
 // them), column tile tn.  Returns false when there is no tile for it.
@@ -1128,11 +1152,13 @@ template <int XT, int NT, int NW, bool SHORT, bool GROUPED> int launch_rows(cons
   if constexpr (NW > 4) {
     if (lds > 160 * 1024) return launch_rows<XT, NT, NW / 2, SHORT, GROUPED>(a, s);
   }
+  // column blocks a workgroup takes: no more workgroups than keep 32 waves on every CU.  Without a k to go
+  // through it takes one (the kernel for several sends for the next block's weights).
   const int64_t blocks = (a.N + 16 * NT - 1) / (16 * NT), active = GROUPED ? std::min(a.E, a.M) : gy;
-  // column blocks a workgroup takes: no more workgroups than keep 32 waves on every CU
-  const int64_t slots = 256 * 32 / NW, share = (blocks * active + slots - 1) / slots;
+  const bool none = a.K == 0 || a.x_rows == 0;
+  const int64_t slots = 256 * 32 / NW, share = none ? 1 : (blocks * active + slots - 1) / slots;
   const dim3 grid((unsigned)((blocks + share - 1) / share), (unsigned)gy);
-  if (grid.x == blocks && a.K <= 512 * NW)
+  if (none || (share == 1 && a.K <= 512 * NW))
     hipLaunchKernelGGL((mx_rows_kernel<XT, NT, NW, SHORT, false, GROUPED>), grid, dim3(NW * 64), lds, s, a);
   else
     hipLaunchKernelGGL((mx_rows_kernel<XT, NT, NW, SHORT, true, GROUPED>), grid, dim3(NW * 64), lds, s, a);
@@ -1151,7 +1177,7 @@ template <int XT, int MI, int NI, int WM, int WN, int RING, bool GROUPED> int la
 
 template <int XT, bool GROUPED> int launch_product(const MxArgs& a, const MxPlan& p, hipStream_t s) {
   if constexpr (XT == FP4) {
-    if (p.tile == 4) return env_int("QMX_W4", 0) ? launch_tiles<XT, 4, 4, 2, 2, 4, GROUPED>(a, s) : launch_tiles<XT, 4, 2, 2, 4, 4, GROUPED>(a, s);
+    if (p.tile == 4) return launch_tiles<XT, 4, 2, 2, 4, 4, GROUPED>(a, s);
     if (p.tile == 3) return launch_tiles<XT, 2, 2, 2, 2, 4, GROUPED>(a, s);
     if (p.tile == 2) return launch_tiles<XT, 1, 2, 2, 2, 4, GROUPED>(a, s);
     if (p.tile == 1) return launch_tiles<XT, 1, 1, 2, 2, 4, GROUPED>(a, s);

@@ -364,7 +364,8 @@ int qmx_dequantize(const uint8_t* codes, const uint8_t* scales, int M, int K, vo
  *   y        [device, out] y_type QG_MX_F16, QG_MX_BF16 or QG_MX_F32, leading dimension ldy >= N.
  * M == 0 or N == 0 is a no-op; K == 0 writes zeros (plus the residual).
  * Sums are added in a fixed order: equal inputs give equal bits.
- * Errors: QG_E_ARG, QG_E_ALIGN, QG_E_UNSUPPORTED (more than 2^31 - 1 tiles), QG_E_DEVICE, QG_E_NOT_DEVICE.
+ * Errors: QG_E_ARG, QG_E_ALIGN, QG_E_UNSUPPORTED (more pieces of y than a grid holds: beyond a
+ * million rows of 16, 64 x 64 pieces beyond 2^31), QG_E_DEVICE, QG_E_NOT_DEVICE.
  */
 int qmx_gemm(const void* x, int ldx, int x_type, const uint8_t* x_scales, const uint8_t* w,
              const uint8_t* w_scales, const void* residual, int ldr, int M, int N, int K, void* y, int ldy,

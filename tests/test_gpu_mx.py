@@ -230,7 +230,75 @@ def test_gemm_equal_inputs_give_equal_bits(kind, M, N, K):
         assert torch.equal(first, qgm.mx_gemm(x, w, ws, x_scales=xs, out_dtype=F32))
 
 
-@pytest.mark.parametrize("M,N,K", [(0, 16, 64), (4, 0, 64), (3, 18, 0)])
+# every kernel whatever the rule would take: sizes around their tiles, K around
+# the stages (128) and groups of them (512), K that ends inside each
+@pytest.mark.parametrize("tile", range(5))
+@pytest.mark.parametrize("kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("M,N,K", [(1, 129, 512), (70, 257, 544), (17, 64, 992), (130, 300, 1024), (260, 70, 1600),
+                                   (3, 40, 128), (66, 130, 352), (5, 17, 32), (129, 513, 480), (33, 100, 2528)])
+def test_gemm_every_kernel(monkeypatch, tile, kind, M, N, K):
+    monkeypatch.setenv("QMX_TILE", str(tile))
+    rng = np.random.default_rng(M + N + K)
+    wc, wsc = random_mx(rng, N, K, spread=0)
+    x, xs, xv = make_x(rng, kind, M, K, exact=True)
+    out = torch.full((M + 1, N), 9.0, dtype=F32, device=DEV)
+    qgm.mx_gemm(x, dev(wc), dev(wsc), x_scales=xs, out=out[:M])
+    assert np.array_equal(f64(out[:M]), mxref.mx_gemm_ref(xv, mxref.mx_values(wc, wsc))[0])
+    assert bool((out[M] == 9).all())
+    # scales of every size, some of them too small or too large for fp16, and a NaN block that only
+    # reaches its own column
+    wsc = rng.integers(95, 150, wsc.shape).astype(np.uint8)
+    wsc[N // 2, -1] = 255
+    x, xs, xv = make_x(rng, kind, M, K)
+    with np.errstate(invalid="ignore"):
+        ref, mag = mxref.mx_gemm_ref(xv, mxref.mx_values(wc, wsc))
+    y = qgm.mx_gemm(x, dev(wc), dev(wsc), x_scales=xs, out_dtype=F32)
+    keep = np.arange(N) != N // 2
+    assert bool(torch.isnan(y[:, N // 2]).all())
+    check(y[:, torch.from_numpy(keep).to(DEV)], ref[:, keep], mag[:, keep], K)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("M", [1, 7, 9, 16])
+@pytest.mark.parametrize("N,K", [(200, 8192), (4200, 4128), (40, 20000)])
+def test_gemm_few_rows_long_k(monkeypatch, kind, M, N, K):
+    # several chunks a wave, x in as much LDS as there is, workgroups with several column blocks
+    monkeypatch.setenv("QMX_TILE", "0")
+    rng = np.random.default_rng(M + K)
+    wc, wsc = random_mx(rng, N, K)
+    x, xs, xv = make_x(rng, kind, M, K)
+    ref, mag = mxref.mx_gemm_ref(xv, mxref.mx_values(wc, wsc))
+    check(qgm.mx_gemm(x, dev(wc), dev(wsc), x_scales=xs, out_dtype=F32), ref, mag, K)
+
+
+@pytest.mark.parametrize("tile", [0, 1, 4])
+@pytest.mark.parametrize("kind", ["bf16", "mx"])
+def test_grouped_far_rows_and_weights(monkeypatch, tile, kind):
+    # rows of x and a matrix that lie more than 4 GiB into their arrays
+    monkeypatch.setenv("QMX_TILE", str(tile))
+    rng = np.random.default_rng(1)
+    E, N, K = 150, 8192, 8192
+    w = torch.zeros(E, N, K // 2, dtype=torch.uint8, device=DEV)
+    ws = torch.full((E, N, K // 32), 120, dtype=torch.uint8, device=DEV)
+    wc, wsc = random_mx(rng, 64, K)
+    w[E - 1, N - 64:], ws[E - 1, N - 64:] = dev(wc), dev(wsc)
+    far = 300000 if kind == "bf16" else 1200000
+    x = torch.zeros(far, K if kind == "bf16" else K // 2, dtype=BF16 if kind == "bf16" else torch.uint8, device=DEV)
+    xs = None if kind == "bf16" else torch.full((far, K // 32), 127, dtype=torch.uint8, device=DEV)
+    few, fews, xv = make_x(rng, kind, 3, K)
+    x[far - 3:] = few
+    if xs is not None:
+        xs[far - 3:] = fews
+    rows = torch.tensor([far - 1, far - 3, 0, far - 2], dtype=torch.int32, device=DEV)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    off[E] = 4
+    y = qgm.mx_gemm_grouped(x, w, ws, off, x_scales=xs, rows=rows, out_dtype=F32)
+    assert not bool(y[:, :N - 64].any()) and not bool(y[2].any())
+    ref, mag = mxref.mx_gemm_ref(xv[[2, 0, 1]], mxref.mx_values(wc, wsc))
+    check(y[[0, 1, 3], N - 64:], ref, mag, K)
+
+
+@pytest.mark.parametrize("M,N,K", [(0, 16, 64), (4, 0, 64), (3, 18, 0), (2, 140000, 0)])
 def test_gemm_empty(M, N, K):
     w = torch.zeros(N, K // 2, dtype=torch.uint8, device=DEV)
     ws = torch.zeros(N, K // 32, dtype=torch.uint8, device=DEV)
@@ -252,10 +320,13 @@ GROUPS = [[1], [3, 0, 5], [0, 0, 40], [16, 1, 0, 31], [1] * 20, [0, 200, 3], [13
           [5] * 70, [0, 0, 0]]
 
 
+@pytest.mark.parametrize("tile", ["", "0", "1", "2", "3", "4"], ids=lambda t: "tile" + t)
 @pytest.mark.parametrize("kind", ["f16", "bf16", "mx"])
 @pytest.mark.parametrize("sizes", GROUPS, ids=lambda s: "-".join(map(str, s[:5])))
 @pytest.mark.parametrize("N,K", [(40, 96), (260, 544)])
-def test_grouped(kind, sizes, N, K):
+def test_grouped(monkeypatch, kind, sizes, N, K, tile):
+    if tile:
+        monkeypatch.setenv("QMX_TILE", tile)
     rng = np.random.default_rng(sum(sizes) + N)
     E, head, behind = len(sizes), 3, 2
     off = make_groups(sizes, head)
@@ -317,6 +388,14 @@ def test_grouped_empty():
     rows = torch.full((5,), -1, dtype=torch.int32, device=DEV)
     y = qgm.mx_gemm_grouped(x, w, ws, off, rows=rows, out=torch.full((5, 16), 9.0, dtype=BF16, device=DEV))
     assert not bool(y.any())
+    # the same where a wave would have work, and many blocks
+    big, bigs = torch.zeros(40, 4000, 512, dtype=torch.uint8, device=DEV), torch.zeros(40, 4000, 32, dtype=torch.uint8, device=DEV)
+    off = torch.arange(41, dtype=torch.int32, device=DEV)
+    y = qgm.mx_gemm_grouped(torch.zeros(0, 1024, dtype=BF16, device=DEV), big, bigs, off,
+                            rows=torch.zeros(40, dtype=torch.int32, device=DEV), out=torch.full((40, 4000), 9.0, dtype=BF16, device=DEV))
+    assert not bool(y.any())
+    off = torch.zeros(4, dtype=torch.int32, device=DEV)
+    x = torch.zeros(0, 64, dtype=BF16, device=DEV)
     # no experts: nothing is written
     y = torch.full((4, 16), 9.0, dtype=BF16, device=DEV)
     qgm.mx_gemm_grouped(x.new_zeros(4, 64), w[:0], ws[:0], off[:1], out=y)

@@ -145,6 +145,31 @@ def test_no_device_status():
     assert grouped() == E_DEVICE and grouped(xr=0, x=None) == E_DEVICE
 
 
+def test_plans(monkeypatch):
+    plan = qgm.mx_plan
+    # few rows: a wave for each chunk of 512 k, at most 16 and what LDS holds
+    assert plan(1, 6144, 2048, F16) == dict(tile=0, blocks=1, waves=4, pieces=384)
+    assert plan(8, 2048, 8192, BF16) == dict(tile=0, blocks=1, waves=16, pieces=128)
+    assert plan(16, 8192, 8192, BF16)["waves"] == 8 and plan(16, 8192, 8192, BF16)["blocks"] == 2
+    assert plan(16, 8192, 8192, FP4)["waves"] == 16
+    assert plan(1, 64, 96, BF16)["waves"] == 1 and plan(1, 64, 0, BF16)["tile"] == 0
+    # larger tiles as the rows grow
+    tiles = [plan(m, 8192, 8192, BF16)["tile"] for m in (1, 64, 512, 4096)]
+    assert tiles[0] == 0 and tiles == sorted(tiles) and tiles[-1] == 4
+    assert plan(4096, 8192, 8192, FP4) == dict(tile=4, blocks=0, waves=0, pieces=512)
+    assert plan(32, 2048, 2048, BF16, groups=32)["tile"] == 0
+    assert plan(16384, 4096, 2048, BF16, groups=32)["tile"] > 1
+    # the rows kernel's grid has 65535 blocks of 16 rows
+    assert plan(1 << 21, 16, 32, BF16)["tile"] > 0
+    for v in range(5):
+        monkeypatch.setenv("QMX_TILE", str(v))
+        assert plan(100, 300, 512, F16)["tile"] == v
+    out = (qgm.ctypes.c_int * 4)()
+    for bad in ((-1, 1, 32, 0, 0), (1, -1, 32, 0, 0), (1, 1, 40, 0, 0), (1, 1, 32, -1, 0), (1, 1, 32, 0, F32)):
+        assert lib.qmx_plan(*bad, out) == E_ARG
+    assert lib.qmx_plan(1, 1, 32, 0, 0, None) == E_ARG
+
+
 def test_binding_refuses_cpu_tensors():
     x = torch.zeros(2, 64, dtype=torch.float16)
     c, s = torch.zeros(2, 32, dtype=torch.uint8), torch.zeros(2, 2, dtype=torch.uint8)
