@@ -419,11 +419,20 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
   uint8_t* const xl = rows_lds + wave * xbytes;
 
   for (int m0 = m_begin; m0 < m_end; m0 += 16) {
-    // what belongs to row m0 + r is loaded first, so that no later wait is for it
+    // what belongs to row m0 + r is loaded first, so that no later wait is for it, and looked at
+    // only when the first weights have been sent for
     const int rows = min(16, m_end - m0), rr = min(r, rows - 1);
-    const int xr = x_row<GROUPED>(a, m0 + r, m_end);
-    const bool has = has_row<GROUPED>(a, m0 + rr);
-    const float factor = GROUPED && a.row_scale ? a.row_scale[m0 + rr] : 1.f;
+    int xr = m0 + rr;
+    float factor = 1.f;
+    if constexpr (GROUPED) {
+      if (a.rows) xr = a.rows[m0 + rr];
+      if (a.row_scale) factor = a.row_scale[m0 + rr];
+    }
+    W w0, w1;
+    int nb = blockIdx.x, turn = 0, buf = 0;
+    if (chunks > 0) load_w(nb, min(wave, chunks - 1), w0);
+    const bool has = xr >= 0 && xr < a.x_rows;
+    xr = has ? xr : 0;
     // x: a whole chunk of the rows there are (past K: a row's last piece again)
     auto load_x = [&](int c) {
       if constexpr (XT == FP4) {
@@ -439,7 +448,6 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
     };
     u4 xs = {0, 0, 0, 0};
     f4 acc[NT];
-    int nb = blockIdx.x, turn = 0, buf = 0;
     const uint8_t* const xsp = XT == FP4 ? a.xs + (int64_t)xr * (a.K >> 5) : nullptr;
     if (turns == 1 && wave < chunks) {
       load_x(wave);
@@ -546,9 +554,7 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
       turn = 0;
       nb += gridDim.x;
     };
-    W w0, w1;
     int left = nb < blocks ? ((blocks - 1 - nb) / (int)gridDim.x + 1) * max(turns, 1) : 0;
-    if (chunks > 0) load_w(nb, min(wave, chunks - 1), w0);
     if constexpr (MULTI) {
       for (; left > 2; left -= 2) {
         item(std::true_type{}, w0, w1);
