@@ -178,6 +178,7 @@ struct MxArgs {
   int64_t ldx_bytes, ldr, ldy;      // x row pitch in bytes, the others in elements
   int x_rows, E, M, N, K;           // M: rows of y (the slots of a grouped product)
   int y_type;
+  int step;                         // mx_rows_kernel: rows at a time, at most 16
 };
 
 // 8 codes -> 8 exact 16-bit values (code times the block's scale)
@@ -355,15 +356,15 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // LDS of a wave for a chunk of x: whole direct loads of a kilobyte (four MXFP4 rows, one 16-bit row)
-template <int XT> __host__ __device__ constexpr int rows_x_bytes(int M) {
-  const int rows = M < 16 ? M : 16;
+template <int XT> __host__ __device__ constexpr int rows_x_bytes(int M, int step) {
+  const int rows = M < step ? M : step;
   return 1024 * (XT == FP4 ? (rows + 3) / 4 : rows);
 }
 
 template <int XT, int NT, int NW, bool SHORT, bool MULTI, bool GROUPED>
 __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
   constexpr int XC = XT == FP4 ? 256 : 1024;     // bytes of an x row a chunk
-  const int xbytes = rows_x_bytes<XT>(a.M);      // a wave's part of the LDS
+  const int xbytes = rows_x_bytes<XT>(a.M, a.step);   // a wave's part of the LDS
   extern __shared__ __align__(1024) uint8_t rows_lds[];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -418,10 +419,10 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
   auto dma = [](const char* from, uint8_t* to) { __builtin_amdgcn_global_load_lds((gptr)from, (lptr)to, 16, 0, 0); };
   uint8_t* const xl = rows_lds + wave * xbytes;
 
-  for (int m0 = m_begin; m0 < m_end; m0 += 16) {
+  for (int m0 = m_begin; m0 < m_end; m0 += a.step) {
     // what belongs to row m0 + r is loaded first, so that no later wait is for it, and looked at
     // only when the first weights have been sent for
-    const int rows = min(16, m_end - m0), rr = min(r, rows - 1);
+    const int rows = min(a.step, m_end - m0), rr = min(r, rows - 1);
     int xr = m0 + rr;
     float factor = 1.f;
     if constexpr (GROUPED) {
@@ -544,7 +545,7 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
 #pragma unroll
         for (int k = 1; k < NW; ++k) v += part[(k * NT + j) * 64 + lane];
         const int m = m0 + r, n = (nb * NT + j) * 16 + 4 * g;
-        if (m < m_end && n < a.N) {
+        if (r < rows && n < a.N) {
           if (!has) v = f4{0.f, 0.f, 0.f, 0.f};
           float o[4] = {v.x, v.y, v.z, v.w};
           store_cols<4>(a, m, n, o, factor);
@@ -1076,7 +1077,7 @@ dim3 ew_grid(int64_t rows, int64_t n8) {
 // and nw waves a workgroup; 1..4: mx_tile_kernel on 64 x 64, 64 x 128, 128 x 128
 // and 256 x 256 tiles (16-bit x: 128 x 256).  QMX_TILE=0..4 in the environment
 // forces one (tests, tuning).
-struct MxPlan { int tile, nt, nw; int64_t workgroups; };
+struct MxPlan { int tile, nt, nw, step; int64_t workgroups; };
 
 // The rule is a model of the time in nanoseconds, from what the kernels
 // measured on graph-replayed products of 1..2048 rows with 2048 and 8192
@@ -1098,7 +1099,7 @@ constexpr MxTileCost MX_TILES[2][4] = {
 
 MxPlan plan_product(int M, int N, int K, int E, int x_type) {
   const bool fp = x_type == FP4;
-  MxPlan p = {0, 1, 1, 0};
+  MxPlan p = {0, 1, 1, 16, 0};
   const int64_t chunks = ((int64_t)K + 511) / 512, stages = ((int64_t)K + 127) / 128;
   const int active = E > 0 ? std::min(E, M) : 1;
   auto row_tiles = [&](int rows) -> int64_t {
@@ -1106,7 +1107,7 @@ MxPlan plan_product(int M, int N, int K, int E, int x_type) {
     return std::max<int64_t>(active, M / rows + active / 2);
   };
   if (K > 0) {
-    const double item = E > 0 ? (fp ? 0.5 : 0.8) : (fp ? 0.9 : 1.7);
+    const double item = E > 0 ? (fp ? 0.5 : M <= 2 * E ? 0.8 : 1.2) : (fp ? 0.9 : 1.7);
     double best = 2300 + item * (double)(row_tiles(16) * (((int64_t)N + 15) / 16) * chunks);
     // a grouped call's workgroups go through their group's rows 16 at a time; some groups are large
     if (E > 0) best += 2500 * (double)(M / (8 * active));
@@ -1127,7 +1128,11 @@ MxPlan plan_product(int M, int N, int K, int E, int x_type) {
     // a wave for every chunk, so that x stays in LDS; where that is more than
     // fits, and x is read again for every block, two blocks share the reading
     p.nw = K < 512 ? 1 : chunks <= 2 ? 2 : chunks <= 4 ? 4 : chunks <= 8 ? 8 : 16;
-    const int rows = std::min(M, 16);
+    // a grouped call of few rows a group: with 8 at a time instead of 16 a 16-bit x takes half the LDS, and
+    // twice the workgroups are resident (32 rows over 32 matrices of 2048 x 2048, bf16: 12.8
+    // us instead of 15.0)
+    if (E > 0 && !fp && M <= 2 * E) p.step = 8;
+    const int rows = std::min(M, p.step);
     const int64_t lds = (int64_t)p.nw * 1024 * ((fp ? (rows + 3) / 4 : rows) + 2);
     if (lds > 160 * 1024) {
       p.nw = 8;
@@ -1154,7 +1159,7 @@ int device_present() {
 template <int XT, int NT, int NW, bool SHORT, bool GROUPED> int launch_rows(const MxArgs& a, hipStream_t s) {
   const int64_t gy = GROUPED ? a.E : ((int64_t)a.M + 15) / 16;
   if (gy > 65535) return QG_E_UNSUPPORTED;
-  const size_t lds = (size_t)NW * rows_x_bytes<XT>(a.M) + 2 * NW * NT * 1024;
+  const size_t lds = (size_t)NW * rows_x_bytes<XT>(a.M, a.step) + 2 * NW * NT * 1024;
   if constexpr (NW > 4) {
     if (lds > 160 * 1024) return launch_rows<XT, NT, NW / 2, SHORT, GROUPED>(a, s);
   }
@@ -1201,7 +1206,7 @@ template <int XT, bool GROUPED> int launch_product(const MxArgs& a, const MxPlan
   return launch_rows<XT, 1, 16, false, GROUPED>(a, s);
 }
 
-template <bool GROUPED> int run_product(const MxArgs& a, int x_type, void* stream) {
+template <bool GROUPED> int run_product(MxArgs& a, int x_type, void* stream) {
   int st = device_present();
   if (st != QG_OK) return st;
   const void* ptrs[9] = {a.x, a.xs, a.w, a.ws, a.rows, a.offsets, a.row_scale, a.resid, a.y};
@@ -1210,6 +1215,7 @@ template <bool GROUPED> int run_product(const MxArgs& a, int x_type, void* strea
   clear_pending_error();
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const MxPlan p = plan_product(a.M, a.N, a.x_rows > 0 ? a.K : 0, GROUPED ? a.E : 0, x_type);
+  a.step = p.step;
   if (x_type == FP4) st = launch_product<FP4, GROUPED>(a, p, s);
   else if (x_type == BF16) st = launch_product<BF16, GROUPED>(a, p, s);
   else st = launch_product<F16, GROUPED>(a, p, s);
