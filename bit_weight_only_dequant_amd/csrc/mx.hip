@@ -364,7 +364,10 @@ template <int XT> __host__ __device__ constexpr int rows_x_bytes(int M, int step
 template <int XT, int NT, int NW, bool SHORT, bool MULTI, bool GROUPED>
 __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
   constexpr int XC = XT == FP4 ? 256 : 1024;     // bytes of an x row a chunk
-  const int xbytes = rows_x_bytes<XT>(a.M, a.step);   // a wave's part of the LDS
+  // Without groups a workgroup has one set of 16 rows, and the constant lets the compiler see that the loop over
+  // rows runs once: with the step from the arguments 1 x 8192 x 8192 took 12.2 us instead of 10.0 (bf16 x).
+  const int step = GROUPED ? a.step : 16;
+  const int xbytes = rows_x_bytes<XT>(a.M, step);   // a wave's part of the LDS
   extern __shared__ __align__(1024) uint8_t rows_lds[];
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -419,10 +422,10 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
   auto dma = [](const char* from, uint8_t* to) { __builtin_amdgcn_global_load_lds((gptr)from, (lptr)to, 16, 0, 0); };
   uint8_t* const xl = rows_lds + wave * xbytes;
 
-  for (int m0 = m_begin; m0 < m_end; m0 += a.step) {
+  for (int m0 = m_begin; m0 < m_end; m0 += step) {
     // what belongs to row m0 + r is loaded first, so that no later wait is for it, and looked at
     // only when the first weights have been sent for
-    const int rows = min(a.step, m_end - m0), rr = min(r, rows - 1);
+    const int rows = min(step, m_end - m0), rr = min(r, rows - 1);
     int xr = m0 + rr;
     float factor = 1.f;
     if constexpr (GROUPED) {
