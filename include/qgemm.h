@@ -354,7 +354,9 @@ int qmx_dequantize(const uint8_t* codes, const uint8_t* scales, int M, int K, vo
 /*
  * qmx_gemm: y[M, N] = x[M, K] . W[N, K]^T (+ residual), W in MXFP4; fp32
  * accumulation and one rounding to y_type at the end.  No element of x or W
- * is rounded on the way: 16-bit x meets the exact weight values.
+ * is rounded on the way: 16-bit x meets the exact weight values.  Those of 2^128 and more (codes of
+ * 2 and up with the scale bytes 253 and 254, which qmx_quantize never writes) are infinite there, so
+ * that their column of y holds infinities or NaN.
  *   x        [device, in] x_type QG_MX_F16 or QG_MX_BF16 with leading dimension ldx >= K, or
  *            QG_MX_FP4: codes (then ldx == K) with x_scales [M, K/32].
  *   x_scales NULL unless x_type is QG_MX_FP4.

@@ -219,6 +219,30 @@ def test_gemm_nan_and_inf_stay_in_their_row_and_column(kind, M, N, K):
     assert (gap[ok_rows][ok[ok_rows]] <= ((K + 3) * 2.0 ** -23 * mag[ok_rows] + 2.0 ** -149)[ok[ok_rows]]).all()
 
 
+# the ends of the scales' range: the smallest make weights down to 2^-128 (16-bit x meets them as subnormal
+# bf16 numbers), 252 is the largest that the quantiser writes.  x keeps the products and sums within fp32's
+# normal numbers, so the tolerance is the usual one.
+@pytest.mark.parametrize("tile", range(5))
+@pytest.mark.parametrize("low", [0, 6, 250])
+@pytest.mark.parametrize("kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("M,N,K", [(3, 40, 96), (20, 70, 1056)])
+def test_gemm_ends_of_the_scales(monkeypatch, tile, low, kind, M, N, K):
+    monkeypatch.setenv("QMX_TILE", str(tile))
+    rng = np.random.default_rng(M + N + low)
+    wc, _ = random_mx(rng, N, K)
+    wsc = rng.integers(low, low + 3, (N, K // 32)).astype(np.uint8)
+    if kind == "mx":
+        x, xs, _ = make_x(rng, kind, M, K)
+        xs = dev(rng.integers(*((150, 160) if low < 250 else (90, 100)), (M, K // 32)).astype(np.uint8))
+        xv = mxref.mx_values(x.cpu().numpy(), xs.cpu().numpy())
+    else:
+        size = (2.0 ** 12 if low < 250 else 2.0 ** -12) if kind == "f16" else (2.0 ** 60 if low < 250 else 2.0 ** -30)
+        x, xs = torch.from_numpy(rng.uniform(1, 2, (M, K)) * size).to(F16 if kind == "f16" else BF16).to(DEV), None
+        xv = f64(x)
+    ref, mag = mxref.mx_gemm_ref(xv, mxref.mx_values(wc, wsc))
+    check(qgm.mx_gemm(x, dev(wc), dev(wsc), x_scales=xs, out_dtype=F32), ref, mag, K)
+
+
 @pytest.mark.parametrize("kind", ["f16", "bf16", "mx"])
 @pytest.mark.parametrize("M,N,K", [(1, 64, 8192), (64, 256, 1024), (512, 512, 1024)])
 def test_gemm_equal_inputs_give_equal_bits(kind, M, N, K):
