@@ -6,23 +6,24 @@
 // Kernels
 //   mx_quantize, mx_dequantize   elementwise, HBM-bound; the device's own fp4
 //                        conversions (round to nearest even, saturating).
-//                        8192 x 8192 bf16 there and back: 60.2 us, 5.05 TB/s
+//                        8192 x 8192 bf16 there and back: 61 us, 5.0 TB/s
 //                        of 304 MB (a large copy reaches 5.14).
 //   mx_rows              few rows.  W and its scales go from memory straight to
 //                        the matrix instruction's registers in their stored
 //                        order, x through LDS; waves split K.  1 x 6144 x 2048
-//                        with fp16 x 5.1 us, 8 x 2048 x 8192 with bf16 x 7 us,
-//                        1 x 8192 x 8192 9.9 us (3.6 TB/s), each in a replayed graph.
+//                        with fp16 x 5.2 us, 8 x 2048 x 8192 with bf16 x 7.2 to
+//                        8.0 us, 1 x 8192 x 8192 with bf16 x 10.0 us (3.6 TB/s),
+//                        each in a replayed graph.
 //   mx_tile              more rows.  x and W through a ring of LDS stages by
-//                        direct loads.  MXFP4 x: 4096 x 8192 x 8192 146 us (3.8
-//                        PFLOP/s); bf16 x: 2048 x 8192 x 8192 228 us (1.2
-//                        PFLOP/s; the library's bf16 product reaches 1.37).
+//                        direct loads.  MXFP4 x: 4096 x 8192 x 8192 142 to 152
+//                        us (3.6 to 3.9 PFLOP/s); bf16 x: 2048 x 8192 x 8192 224
+//                        us (1.23 PFLOP/s; the library's bf16 product reaches 1.37).
 // The stored form needs no packing step: 16 consecutive bytes of a row are one
 // block of 32, which is what one lane supplies to v_mfma_scale_f32_16x16x128 and
 // 32x32x64 (fp4 operands, one scale byte a lane), so the products read
 // checkpoints' own layout.
 // Precision.  MXFP4 values meet 16-bit x exactly: code times scale is an exact
-// bf16 number, so bf16 x uses bf16 matrix instructions and loses nothing; with
+// bf16 number below 2^128 (subnormal for the smallest scales), so bf16 x uses bf16 matrix instructions and loses nothing; with
 // fp16 x it is an exact fp16 number for scales of 2^-23 .. 2^8, and where a wave
 // meets others it multiplies bf16 weights with x split in two exact bf16 parts.
 // Sums are fp32; the one rounding is at the store.
@@ -580,7 +581,7 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
 // ---------------------------------------------------------------------------
 // Where a workgroup's tile lies: group e, rows m0 .. m_end of y (at most TM of
 // them), column tile tn.  Returns false when there is no tile for it.
-// Tiles are numbered n fastest within blocks of 8 row tiles, and a number range
+// Tiles are numbered row tile fastest within blocks of 8 row tiles, and a number range
 // goes to one XCD (workgroup b runs on XCD b % 8), so the tiles whose operands
 // an XCD's L2 holds run together.  A grouped product finds its row tiles from
 // the offsets: lane by lane the tiles of 64 groups, a running sum, a vote.
@@ -1091,9 +1092,9 @@ struct MxPlan { int tile, nt, nw, step; int64_t workgroups; };
 // further tile of the CU.  The rows kernel takes `item` for a block of 16 x 16
 // outputs and chunk of 512 k, over the whole chip, and a pause between 16 rows
 // of a group and the next.  For instance 8192 x 8192
-// weights and bf16 x: 16 rows 13.3 us (64 x 64 tiles 24.8), 64 rows on 64 x 64
-// tiles 24.9 (rows kernel 42), 512 rows on 128 x 128 66 (64 x 64 88, 128 x 256
-// 88), 2048 rows on 128 x 256 233 (128 x 128 273).  How many row tiles a
+// weights and bf16 x: 16 rows 13.4 us (64 x 64 tiles 21.4), 64 rows on 64 x 64
+// tiles 21.6 (rows kernel 42), 512 rows on 128 x 128 66 (64 x 64 96, 128 x 256
+// 87), 2048 rows on 128 x 256 224 (128 x 128 258).  How many row tiles a
 // grouped product has is estimated: each group's last one half empty.
 struct MxTileCost { int rows, cols; double alone, shared, start, more; };
 constexpr MxTileCost MX_TILES[2][4] = {
