@@ -1104,6 +1104,7 @@ constexpr MxTileCost MX_TILES[2][4] = {
 MxPlan plan_product(int M, int N, int K, int E, int x_type) {
   const bool fp = x_type == FP4;
   MxPlan p = {0, 1, 1, 16, 0};
+  if (M == 0 || N == 0) return p;   // nothing to launch; below, a grouped call has at least one active group
   const int64_t chunks = ((int64_t)K + 511) / 512, stages = ((int64_t)K + 127) / 128;
   const int active = E > 0 ? std::min(E, M) : 1;
   auto row_tiles = [&](int rows) -> int64_t {
@@ -1114,7 +1115,7 @@ MxPlan plan_product(int M, int N, int K, int E, int x_type) {
     const double item = E > 0 ? (fp ? 0.5 : M <= 2 * E ? 0.8 : 1.2) : (fp ? 0.9 : 1.7);
     double best = 2300 + item * (double)(row_tiles(16) * (((int64_t)N + 15) / 16) * chunks);
     // a grouped call's workgroups go through their group's rows 16 at a time; some groups are large
-    if (E > 0) best += 2500 * (double)(M / (8 * active));
+    if (E > 0) best += 2500 * (double)(M / (8 * (int64_t)active));
     if (row_tiles(16) > 65535) best = 1e300;   // the rows kernel's grid
     int64_t tiles[4];
     for (int i = 0; i < 4; ++i) {
@@ -1259,6 +1260,7 @@ using namespace qg;
 
 extern "C" int qmx_plan(int M, int N, int K, int E, int x_type, int out[4]) {
   if (M < 0 || N < 0 || K < 0 || E < 0 || K % 32 || (x_type != F16 && x_type != BF16 && x_type != FP4) || !out) return QG_E_ARG;
+  if (E > 65535 || M > INT_MAX - 512 || N > INT_MAX - 512) return QG_E_UNSUPPORTED;   // as the products
   const MxPlan p = plan_product(M, N, K, E, x_type);
   out[0] = p.tile;
   out[1] = p.tile ? 0 : p.nt;

@@ -170,6 +170,25 @@ def test_plans(monkeypatch):
     assert lib.qmx_plan(1, 1, 32, 0, 0, None) == E_ARG
 
 
+@pytest.mark.parametrize("x_type", [F16, BF16, FP4])
+@pytest.mark.parametrize("groups", [0, 1, 4, 65535])
+@pytest.mark.parametrize("M,N", [(0, 16), (16, 0), (0, 0)])
+def test_plan_of_nothing(M, N, groups, x_type):
+    for K in (0, 64, 8192):
+        assert qgm.mx_plan(M, N, K, x_type, groups=groups) == dict(tile=0, blocks=1, waves=1, pieces=0)
+
+
+def test_plan_limits():
+    # what the products refuse by their sizes alone; the largest they take has a plan, grouped or not
+    out = (qgm.ctypes.c_int * 4)()
+    top = (1 << 31) - 1
+    for bad in ((1 << 29, 16, 64, 1 << 29, BF16), (1, 16, 64, 65536, F16), (top, 16, 64, 0, FP4), (16, top, 64, 0, F16)):
+        assert lib.qmx_plan(*bad, out) == E_UNSUP
+    for M, E in ((1, 65535), (1 << 29, 65535), (top - 512, 65535), (top - 512, 1), (top - 512, 0)):
+        for x_type in (F16, BF16, FP4):
+            assert lib.qmx_plan(M, 16, 64, E, x_type, out) == OK and out[3] > 0
+
+
 def test_binding_refuses_cpu_tensors():
     x = torch.zeros(2, 64, dtype=torch.float16)
     c, s = torch.zeros(2, 32, dtype=torch.uint8), torch.zeros(2, 2, dtype=torch.uint8)
