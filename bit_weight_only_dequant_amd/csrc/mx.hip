@@ -550,7 +550,10 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
         for (int k = 1; k < NW; ++k) v += part[(k * NT + j) * 64 + lane];
         const int m = m0 + r, n = (nb * NT + j) * 16 + 4 * g;
         if (r < rows && n < a.N) {
-          if (!has) v = f4{0.f, 0.f, 0.f, 0.f};
+          if (!has) {   // zero whatever the slot's factor holds: a padding slot's may be unset
+            v = f4{0.f, 0.f, 0.f, 0.f};
+            factor = 1.f;
+          }
           float o[4] = {v.x, v.y, v.z, v.w};
           store_cols<4>(a, m, n, o, factor);
         }
@@ -747,8 +750,10 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
   const int nkb = a.K >> 5;
 
   if constexpr (GROUPED) {
-    for (int i = tid; i < t.m_end - t.m0; i += NW * 64)
-      info[i] = f2{a.row_scale ? a.row_scale[t.m0 + i] : 1.f, has_row<true>(a, t.m0 + i) ? 1.f : 0.f};
+    for (int i = tid; i < t.m_end - t.m0; i += NW * 64) {
+      const bool has = has_row<true>(a, t.m0 + i);   // without a row: zero whatever the slot's factor holds
+      info[i] = f2{a.row_scale && has ? a.row_scale[t.m0 + i] : 1.f, has ? 1.f : 0.f};
+    }
   }
   // direct loads: lane l brings a 16-byte chunk of row l / 4 of 16 (16-bit x: row l / 16 of 4)
   const char* src[QD];

@@ -380,7 +380,8 @@ int qmx_gemm(const void* x, int ldx, int x_type, const uint8_t* x_scales, const 
  *   y[t, :] = row_scale[t] * (x[rows[t], :] . W[e]^T)   for offsets[e] <= t < offsets[e + 1].
  *   x, x_scales as qmx_gemm, with x_rows rows.
  *   rows      [device, in] int32 [T]: the row of x that slot t takes; a value outside [0, x_rows)
- *             makes the slot's output row zero.  NULL: slot t takes row t (then x_rows >= T).
+ *             makes the slot's output row zero, whatever its row_scale holds.  NULL: slot t takes
+ *             row t (then x_rows >= T).
  *   w, w_scales [device, in] MXFP4 [E, N, K].
  *   offsets   [device, in] int32 [E + 1], not decreasing, within [0, T].  They are read on the
  *             device: nothing waits for them on the host.  Whatever they hold, no access leaves

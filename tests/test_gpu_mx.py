@@ -426,6 +426,36 @@ def test_grouped_empty():
     assert bool((y == 9).all())
 
 
+@pytest.mark.parametrize("tile", range(5))
+@pytest.mark.parametrize("kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("N,K", [(40, 96), (260, 544), (40, 0)])
+def test_grouped_slots_without_a_row_are_zero_whatever_their_factor(monkeypatch, kind, N, K, tile):
+    # a padded batch: the padding slots' factors were never written
+    monkeypatch.setenv("QMX_TILE", str(tile))
+    rng = np.random.default_rng(N + K)
+    sizes = [7, 0, 40, 1, 130]
+    off, E, T, xr = make_groups(sizes), len(sizes), sum(sizes), 50
+    rows = rng.integers(0, xr, T).astype(np.int32)
+    pad = rng.random(T) < 0.4
+    pad[:2] = True
+    rows[pad] = rng.choice(np.array([-1, xr, -2147483648, 2147483647], dtype=np.int32), int(pad.sum()))
+    scale = rng.standard_normal(T).astype(np.float32)
+    scale[pad] = rng.choice(np.array([np.nan, np.inf, -np.inf, -1.0, 2.0], dtype=np.float32), int(pad.sum()))
+    x, xs, xv = make_x(rng, kind, xr, K)
+    wc, wsc = random_mx(rng, E * N, K)
+    w, ws = dev(wc.reshape(E, N, K // 2)), dev(wsc.reshape(E, N, K // 32))
+    out = torch.full((T, N), 9.0, dtype=F32, device=DEV)
+    qgm.mx_gemm_grouped(x, w, ws, dev(off), x_scales=xs, rows=dev(rows), row_scale=dev(scale), out=out)
+    assert not out[dev(pad)].view(torch.int32).any()          # +0 in every bit
+    ref, mag = mxref.mx_grouped_ref(xv, mxref.mx_values(wc, wsc).reshape(E, N, K), off, rows, scale)
+    check(out, ref, mag, K)
+    # no rows of x at all
+    out.fill_(9.0)
+    none = x[:0], None if xs is None else xs[:0]
+    qgm.mx_gemm_grouped(none[0], w, ws, dev(off), x_scales=none[1], rows=dev(rows), row_scale=dev(scale), out=out)
+    assert not out.view(torch.int32).any()
+
+
 # -------------------------------------------- as used together, graphs, streams
 
 def moe(x, up, down, offsets, rows, scale):
