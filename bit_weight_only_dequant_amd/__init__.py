@@ -474,6 +474,14 @@ def _mx_stream(dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _mx_int(what, *sizes):
+    """Refuses sizes and strides that the library's 32-bit arguments cannot
+    hold: ctypes would pass their low 32 bits."""
+    for v in sizes:
+        if v > 0x7fffffff:
+            raise ValueError(f"{what}: {v} is beyond {0x7fffffff}, the largest size or stride")
+
+
 def _mx_float(t, what, dev, shape=None, types=_MX_TYPE):
     """A 2-d floating tensor with unit column stride -> (its type, its row stride)."""
     xt, sh = types.get(t.dtype), t.shape
@@ -483,7 +491,11 @@ def _mx_float(t, what, dev, shape=None, types=_MX_TYPE):
     row, col = t.stride()
     if col != 1 and sh[1] > 1:
         raise ValueError(f"{what} must have unit column stride")
-    return xt, row if sh[0] > 1 else sh[1]
+    if sh[0] <= 1:
+        row = sh[1]
+    if (sh[0] | sh[1] | row) >> 31:
+        _mx_int(what, *sh, row)
+    return xt, row
 
 
 def _mx_matrix(codes, scales, what, dev, dims=2):
@@ -492,6 +504,8 @@ def _mx_matrix(codes, scales, what, dev, dims=2):
     if (codes.dtype is _U8 and scales.dtype is _U8 and len(sh) == dims and sh[-1] % 16 == 0
             and scales.shape == (*sh[:-1], sh[-1] // 16) and codes.get_device() == dev and scales.get_device() == dev
             and codes.is_contiguous() and scales.is_contiguous()):
+        if (sh[0] | sh[-2] | 2 * sh[-1]) >> 31:
+            _mx_int(what, *sh, 2 * sh[-1])
         return sh
     raise ValueError(f"{what} must be contiguous uint8 codes [{'.., ' * (dims - 2)}R, K/2] and scales of as many rows and "
                      f"K/32 columns, K a multiple of {MX_BLOCK}, on GPU {dev}; got {codes.dtype} {list(sh)} on "
@@ -626,6 +640,8 @@ def mx_gemm_grouped(x, w, w_scales, offsets, x_scales=None, rows=None, row_scale
     rp = sp = None
     if rows is not None:
         T = rows.numel()
+        if T >> 31:
+            _mx_int("rows", T)
         rp = _mx_vector(rows, _I32, T, "rows", dev)
     if row_scale is not None:
         sp = _mx_vector(row_scale, _F32, T, "row_scale", dev)
@@ -640,6 +656,7 @@ def mx_gemm_grouped(x, w, w_scales, offsets, x_scales=None, rows=None, row_scale
 def mx_plan(M: int, N: int, K: int, x_type: int, groups: int = 0) -> dict:
     """The kernel an MXFP4 product takes; see qmx_plan."""
     out = (_I * 4)()
+    _mx_int("plan", M, N, K, groups)
     _check(_lib.qmx_plan(M, N, K, groups, x_type, out), "qmx_plan")
     return dict(tile=out[0], blocks=out[1], waves=out[2], pieces=out[3])
 

@@ -456,6 +456,26 @@ def test_grouped_slots_without_a_row_are_zero_whatever_their_factor(monkeypatch,
     assert not out.view(torch.int32).any()
 
 
+def test_strides_and_sizes_past_32_bits_are_refused():
+    # one allocation of 8.6 GB: a far second row, and a row longer than 2^31
+    far = (1 << 32) + 64
+    flat = torch.empty(far + 64, dtype=F16, device=DEV)
+    x, long_row = flat.as_strided((2, 64), (far, 1)), flat[:far].view(1, far)
+    w, ws = torch.zeros(64, 32, dtype=torch.uint8, device=DEV), torch.zeros(64, 2, dtype=torch.uint8, device=DEV)
+    few, off = torch.zeros(2, 64, dtype=F16, device=DEV), torch.tensor([0, 2], dtype=torch.int32, device=DEV)
+    for call in (lambda: qgm.mx_quantize(x), lambda: qgm.mx_quantize(long_row),
+                 lambda: qgm.mx_dequantize(w[:2], ws[:2], out=x), lambda: qgm.mx_gemm(x, w, ws),
+                 lambda: qgm.mx_gemm(few, w, ws, out=x), lambda: qgm.mx_gemm(few, w, ws, residual=x),
+                 lambda: qgm.mx_gemm_grouped(x, w[None], ws[None], off),
+                 lambda: qgm.mx_gemm_grouped(few, w[None], ws[None], off, out=x)):
+        with pytest.raises(ValueError, match="2147483647"):
+            call()
+    # one row has no stride that counts
+    x = flat.as_strided((1, 64), (far, 1))
+    x.normal_()
+    assert torch.equal(qgm.mx_gemm(x, w, ws), x.new_zeros(1, 64))
+
+
 # -------------------------------------------- as used together, graphs, streams
 
 def moe(x, up, down, offsets, rows, scale):

@@ -189,6 +189,51 @@ def test_plan_limits():
             assert lib.qmx_plan(M, 16, 64, E, x_type, out) == OK and out[3] > 0
 
 
+def test_binding_refuses_sizes_and_strides_past_32_bits(monkeypatch):
+    """Before the library is called: a stride, a number of rows or a length that 32 bits cut off would read as a
+    small one there.  Tensors without memory stand for the large ones."""
+    class Never:
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} was called")
+    monkeypatch.setattr(qgm, "_lib", Never())
+    monkeypatch.setattr(qgm, "_mx_elsewhere", lambda x, stream: None)
+    monkeypatch.setattr(qgm, "_dev", lambda t, what: t)
+
+    def t(shape, dtype=torch.float16, stride=None):
+        return torch.empty_strided(shape, stride or [int(np.prod(shape[i + 1:])) for i in range(len(shape))],
+                                   dtype=dtype, device="meta")
+    u8, i32, f32 = torch.uint8, torch.int32, torch.float32
+
+    def mx(*shape):
+        return t((*shape[:-1], shape[-1] // 2), u8), t((*shape[:-1], shape[-1] // 32), u8)
+    big = 1 << 32
+    few, far, many, wide = t((2, 64)), t((2, 64), stride=(big + 64, 1)), t((big + 2, 64)), t((1, big + 64))
+    w, ws = mx(64, 64)
+    gw, gs = mx(3, 64, 64)
+    off = t((4,), i32)
+    calls = [
+        lambda: qgm.mx_quantize(far), lambda: qgm.mx_quantize(many), lambda: qgm.mx_quantize(wide),
+        lambda: qgm.mx_quantize(t((2, 64), stride=(1 << 31, 1))), lambda: qgm.mx_quantize(t((1 << 31, 64))),
+        lambda: qgm.mx_dequantize(*mx(2, 64), out=far), lambda: qgm.mx_dequantize(*mx(big + 2, 64)),
+        lambda: qgm.mx_dequantize(*mx(1, big + 64)),
+        lambda: qgm.mx_gemm(far, w, ws), lambda: qgm.mx_gemm(many, w, ws), lambda: qgm.mx_gemm(few, w, ws, out=far),
+        lambda: qgm.mx_gemm(few, w, ws, residual=far), lambda: qgm.mx_gemm(few, *mx(big + 3, 64)),
+        lambda: qgm.mx_gemm(wide, *mx(3, big + 64)), lambda: qgm.mx_gemm(mx(big + 2, 64)[0], w, ws, x_scales=mx(big + 2, 64)[1]),
+        lambda: qgm.mx_gemm_grouped(far, gw, gs, off), lambda: qgm.mx_gemm_grouped(many, gw, gs, off),
+        lambda: qgm.mx_gemm_grouped(few, gw, gs, off, out=far), lambda: qgm.mx_gemm_grouped(few, gw, gs, off, rows=t((big + 2,), i32)),
+        lambda: qgm.mx_gemm_grouped(few, *mx(big + 3, 0, 64), t((big + 4,), i32)),
+        lambda: qgm.MXLinear(*mx(big + 3, 64)),
+        lambda: qgm.mx_plan(big + 1, 16, 64, BF16), lambda: qgm.mx_plan(1, big + 16, 64, BF16),
+        lambda: qgm.mx_plan(1, 16, big + 64, BF16), lambda: qgm.mx_plan(1, 16, 64, BF16, groups=big + 1),
+    ]
+    for call in calls:
+        with pytest.raises(ValueError, match="2147483647"):
+            call()
+    monkeypatch.undo()
+    with pytest.raises(qgm.QGemmError):
+        qgm.mx_plan(-1, 16, 64, BF16)
+
+
 def test_binding_refuses_cpu_tensors():
     x = torch.zeros(2, 64, dtype=torch.float16)
     c, s = torch.zeros(2, 32, dtype=torch.uint8), torch.zeros(2, 2, dtype=torch.uint8)
