@@ -18,6 +18,7 @@
 //                        direct loads.  MXFP4 x: 4096 x 8192 x 8192 142 to 152
 //                        us (3.6 to 3.9 PFLOP/s); bf16 x: 2048 x 8192 x 8192 224
 //                        us (1.23 PFLOP/s; the library's bf16 product reaches 1.37).
+//   mx_no_k              a product without a k: the residual, or zeros.
 // The stored form needs no packing step: 16 consecutive bytes of a row are one
 // block of 32, which is what one lane supplies to v_mfma_scale_f32_16x16x128 and
 // 32x32x64 (fp4 operands, one scale byte a lane), so the products read
@@ -1061,6 +1062,17 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
   store_blocks<MI, NI, GROUPED>(a, t, smem + wave * (32 * (32 * NI + 4) * 4), wm * MI * 32, n0 + wn * NI * 32, info, acc);
 }
 
+// A product without a k, one element a lane: the residual, or zero.
+template <int YT> __global__ __launch_bounds__(EW_THREADS) void mx_no_k_kernel(MxArgs a) {
+  typedef typename Elem<YT>::type E;
+  const int64_t step = (int64_t)gridDim.x * EW_THREADS, n = (int64_t)a.M * a.N;
+  for (int64_t i = (int64_t)blockIdx.x * EW_THREADS + threadIdx.x; i < n; i += step) {
+    const int64_t row = i / a.N, col = i - row * a.N;
+    const float r = a.resid ? to_f32(reinterpret_cast<const E*>(a.resid)[row * a.ldr + col]) : 0.f;
+    reinterpret_cast<E*>(a.y)[row * a.ldy + col] = (E)(0.f + r);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -1173,10 +1185,10 @@ template <int XT, int NT, int NW, bool SHORT, bool GROUPED> int launch_rows(cons
   if constexpr (NW > 4) {
     if (lds > 160 * 1024) return launch_rows<XT, NT, NW / 2, SHORT, GROUPED>(a, s);
   }
-  // column blocks a workgroup takes: no more workgroups than keep 32 waves on every CU.  Without a k to go
-  // through it takes one (the kernel for several sends for the next block's weights).
+  // column blocks a workgroup takes: no more workgroups than keep 32 waves on every CU.  A grouped product
+  // without a k to go through takes one (the kernel for several sends for the next block's weights).
   const int64_t blocks = (a.N + 16 * NT - 1) / (16 * NT), active = GROUPED ? std::min(a.E, a.M) : gy;
-  const bool none = a.K == 0 || a.x_rows == 0;
+  const bool none = GROUPED && (a.K == 0 || a.x_rows == 0);
   const int64_t slots = 256 * 32 / NW, share = none ? 1 : (blocks * active + slots - 1) / slots;
   const dim3 grid((unsigned)((blocks + share - 1) / share), (unsigned)gy);
   if (none || (share == 1 && a.K <= 512 * NW))
@@ -1216,6 +1228,13 @@ template <int XT, bool GROUPED> int launch_product(const MxArgs& a, const MxPlan
   return launch_rows<XT, 1, 16, false, GROUPED>(a, s);
 }
 
+void launch_no_k(const MxArgs& a, hipStream_t s) {
+  const dim3 grid = ew_grid(1, (int64_t)a.M * a.N), block(EW_THREADS);
+  if (a.y_type == F32) hipLaunchKernelGGL(mx_no_k_kernel<F32>, grid, block, 0, s, a);
+  else if (a.y_type == F16) hipLaunchKernelGGL(mx_no_k_kernel<F16>, grid, block, 0, s, a);
+  else hipLaunchKernelGGL(mx_no_k_kernel<BF16>, grid, block, 0, s, a);
+}
+
 template <bool GROUPED> int run_product(MxArgs& a, int x_type, void* stream) {
   int st = device_present();
   if (st != QG_OK) return st;
@@ -1224,6 +1243,10 @@ template <bool GROUPED> int run_product(MxArgs& a, int x_type, void* stream) {
   if (st != QG_OK) return st;
   clear_pending_error();
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (!GROUPED && a.K == 0) {
+    launch_no_k(a, s);
+    return launch_status();
+  }
   const MxPlan p = plan_product(a.M, a.N, a.x_rows > 0 ? a.K : 0, GROUPED ? a.E : 0, x_type);
   a.step = p.step;
   if (x_type == FP4) st = launch_product<FP4, GROUPED>(a, p, s);

@@ -402,7 +402,7 @@ int qmx_gemm_grouped(const void* x, int ldx, int x_type, const uint8_t* x_scales
  * 64 x 128, 128 x 128 or 256 x 256 (16-bit x: 128 x 256) outputs; out[1],
  * out[2] = column blocks of 16 and waves a workgroup of the former; out[3] =
  * pieces of y (an estimate where grouped).  QMX_TILE=0..4 in the environment
- * forces out[0].  M == 0 or N == 0: all zero but out[1] and out[2], which are 1.
+ * forces out[0].  K == 0 without groups has an elementwise kernel of its own and is told as 0.  M == 0 or N == 0: all zero but out[1] and out[2], which are 1.
  * Errors: QG_E_ARG, QG_E_UNSUPPORTED (M, N or E beyond what the products take). */
 int qmx_plan(int M, int N, int K, int E, int x_type, int out[4]);
 

@@ -476,6 +476,22 @@ def test_strides_and_sizes_past_32_bits_are_refused():
     assert torch.equal(qgm.mx_gemm(x, w, ws), x.new_zeros(1, 64))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "mx"])
+@pytest.mark.parametrize("yt", [F16, BF16, F32])
+@pytest.mark.parametrize("M,N", [(65535 * 16 + 5, 3), (1, 140001), (37, 70), (2100000, 1)])
+def test_gemm_without_k_of_any_size(kind, yt, M, N):
+    w, ws = torch.zeros(N, 0, dtype=torch.uint8, device=DEV), torch.zeros(N, 0, dtype=torch.uint8, device=DEV)
+    x, xs = (torch.zeros(M, 0, dtype=BF16, device=DEV), None) if kind == "bf16" else (w.new_zeros(M, 0), w.new_zeros(M, 0))
+    r = torch.randn(M, N + 5, device=DEV).to(yt)[:, :N]
+    out = torch.full((M + 1, N + 2), 9.0, dtype=yt, device=DEV)
+    for res in (None, r):
+        qgm.mx_gemm(x, w, ws, x_scales=xs, out=out[:M, :N], residual=res)
+        assert torch.equal(out[:M, :N], torch.zeros_like(r) if res is None else r)
+    assert bool((out[:M, N:] == 9).all()) and bool((out[M] == 9).all())
+    qgm.mx_gemm(x, w, ws, x_scales=xs, out=out[:M, :N], residual=out[:M, :N])   # in place
+    assert torch.equal(out[:M, :N], r)
+
+
 # -------------------------------------------- as used together, graphs, streams
 
 def moe(x, up, down, offsets, rows, scale):
