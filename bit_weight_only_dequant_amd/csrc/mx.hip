@@ -1098,7 +1098,9 @@ dim3 ew_grid(int64_t rows, int64_t n8) {
 // and nw waves a workgroup; 1..4: mx_tile_kernel on 64 x 64, 64 x 128, 128 x 128
 // and 256 x 256 tiles (16-bit x: 128 x 256).  QMX_TILE=0..4 in the environment
 // forces one (tests, tuning).
-struct MxPlan { int tile, nt, nw, step; int64_t workgroups; };
+// fits: whether a grid holds it (65535 blocks along y, and along x 2^32 - 1
+// lanes).
+struct MxPlan { int tile, nt, nw, step; int64_t workgroups; bool fits; };
 
 // The rule is a model of the time in nanoseconds, from what the kernels
 // measured on graph-replayed products of 1..2048 rows with 2048 and 8192
@@ -1113,14 +1115,23 @@ struct MxPlan { int tile, nt, nw, step; int64_t workgroups; };
 // tiles 21.6 (rows kernel 42), 512 rows on 128 x 128 66 (64 x 64 96, 128 x 256
 // 87), 2048 rows on 128 x 256 224 (128 x 128 258).  How many row tiles a
 // grouped product has is estimated: each group's last one half empty.
-struct MxTileCost { int rows, cols; double alone, shared, start, more; };
+struct MxTileCost { int rows, cols, threads; double alone, shared, start, more; };
 constexpr MxTileCost MX_TILES[2][4] = {
-    {{64, 64, 385, 345, 3000, 0.3}, {64, 128, 490, 510, 3200, 0.5}, {128, 128, 770, 1030, 3500, 0.5}, {128, 256, 1290, 1730, 4000, 0.8}},
-    {{64, 64, 165, 180, 2900, 0.3}, {64, 128, 215, 255, 3000, 0.8}, {128, 128, 265, 390, 3300, 0.4}, {256, 256, 720, 1130, 5500, 1.0}}};
+    {{64, 64, 256, 385, 345, 3000, 0.3}, {64, 128, 256, 490, 510, 3200, 0.5},
+     {128, 128, 512, 770, 1030, 3500, 0.5}, {128, 256, 512, 1290, 1730, 4000, 0.8}},
+    {{64, 64, 256, 165, 180, 2900, 0.3}, {64, 128, 256, 215, 255, 3000, 0.8},
+     {128, 128, 256, 265, 390, 3300, 0.4}, {256, 256, 512, 720, 1130, 5500, 1.0}}};
+
+// Workgroups of a tiled product (E = 0: not grouped): a grouped one has at
+// most this many row tiles, whatever its offsets hold.
+int64_t tile_grid(int M, int N, int E, int rows, int cols) {
+  const int64_t tm = E > 0 ? M / rows + std::min(E, M) : ((int64_t)M + rows - 1) / rows;
+  return (((int64_t)N + cols - 1) / cols * tm + 7) / 8 * 8;
+}
 
 MxPlan plan_product(int M, int N, int K, int E, int x_type) {
   const bool fp = x_type == FP4;
-  MxPlan p = {0, 1, 1, 16, 0};
+  MxPlan p = {0, 1, 1, 16, 0, true};
   if (M == 0 || N == 0) return p;   // nothing to launch; below, a grouped call has at least one active group
   const int64_t chunks = ((int64_t)K + 511) / 512, stages = ((int64_t)K + 127) / 128;
   const int active = E > 0 ? std::min(E, M) : 1;
@@ -1146,7 +1157,12 @@ MxPlan plan_product(int M, int N, int K, int E, int x_type) {
     if (forced >= 0 && forced <= 4) p.tile = forced;
     if (p.tile) p.workgroups = tiles[p.tile - 1];
   }
-  if (p.tile == 0) {
+  if (p.tile) {
+    const MxTileCost& c = MX_TILES[fp][p.tile - 1];
+    p.fits = tile_grid(M, N, E, c.rows, c.cols) * c.threads <= (int64_t)UINT32_MAX;
+  } else {
+    // without a k: a workgroup of one wave for every block of a group's columns; without groups another kernel
+    p.fits = E > 0 ? K > 0 || ((int64_t)N + 15) / 16 * 64 <= (int64_t)UINT32_MAX : K == 0 || row_tiles(16) <= 65535;
     // a wave for every chunk, so that x stays in LDS; where that is more than
     // fits, and x is read again for every block, two blocks share the reading
     p.nw = K < 512 ? 1 : chunks <= 2 ? 2 : chunks <= 4 ? 4 : chunks <= 8 ? 8 : 16;
@@ -1180,7 +1196,6 @@ int device_present() {
 
 template <int XT, int NT, int NW, bool SHORT, bool GROUPED> int launch_rows(const MxArgs& a, hipStream_t s) {
   const int64_t gy = GROUPED ? a.E : ((int64_t)a.M + 15) / 16;
-  if (gy > 65535) return QG_E_UNSUPPORTED;
   const size_t lds = (size_t)NW * rows_x_bytes<XT>(a.M, a.step) + 2 * NW * NT * 1024;
   if constexpr (NW > 4) {
     if (lds > 160 * 1024) return launch_rows<XT, NT, NW / 2, SHORT, GROUPED>(a, s);
@@ -1188,7 +1203,7 @@ template <int XT, int NT, int NW, bool SHORT, bool GROUPED> int launch_rows(cons
   // column blocks a workgroup takes: no more workgroups than keep 32 waves on every CU.  A grouped product
   // without a k to go through takes one (the kernel for several sends for the next block's weights).
   const int64_t blocks = (a.N + 16 * NT - 1) / (16 * NT), active = GROUPED ? std::min(a.E, a.M) : gy;
-  const bool none = GROUPED && (a.K == 0 || a.x_rows == 0);
+  const bool none = GROUPED && SHORT && (a.K == 0 || a.x_rows == 0);
   const int64_t slots = 256 * 32 / NW, share = none ? 1 : (blocks * active + slots - 1) / slots;
   const dim3 grid((unsigned)((blocks + share - 1) / share), (unsigned)gy);
   if (none || (share == 1 && a.K <= 512 * NW))
@@ -1200,11 +1215,8 @@ template <int XT, int NT, int NW, bool SHORT, bool GROUPED> int launch_rows(cons
 
 template <int XT, int MI, int NI, int WM, int WN, int RING, bool GROUPED> int launch_tiles(const MxArgs& a, hipStream_t s) {
   constexpr int TM = 32 * MI * WM, TN = 32 * NI * WN;
-  const int64_t tn = (a.N + TN - 1) / TN;
-  const int64_t tm = GROUPED ? a.M / TM + std::min(a.E, a.M) : (a.M + TM - 1) / TM;   // at most
-  const int64_t grid = (tn * tm + 7) / 8 * 8;
-  if (grid > INT_MAX) return QG_E_UNSUPPORTED;
-  hipLaunchKernelGGL((mx_tile_kernel<XT, MI, NI, WM, WN, RING, GROUPED>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, s, a, (int)tn);
+  const dim3 grid((unsigned)tile_grid(a.M, a.N, GROUPED ? a.E : 0, TM, TN));
+  hipLaunchKernelGGL((mx_tile_kernel<XT, MI, NI, WM, WN, RING, GROUPED>), grid, dim3(WM * WN * 64), 0, s, a, (a.N + TN - 1) / TN);
   return QG_OK;
 }
 
@@ -1220,7 +1232,7 @@ template <int XT, bool GROUPED> int launch_product(const MxArgs& a, const MxPlan
     if (p.tile == 2) return launch_tiles<XT, 2, 1, 1, 4, 3, GROUPED>(a, s);
     if (p.tile == 1) return launch_tiles<XT, 1, 1, 2, 2, 3, GROUPED>(a, s);
   }
-  if (a.K < 512) return launch_rows<XT, 1, 1, true, GROUPED>(a, s);
+  if (a.K < 512 || a.x_rows == 0) return launch_rows<XT, 1, 1, true, GROUPED>(a, s);
   if (p.nt == 2) return launch_rows<XT, 2, 8, false, GROUPED>(a, s);
   if (p.nw == 2) return launch_rows<XT, 1, 2, false, GROUPED>(a, s);
   if (p.nw == 4) return launch_rows<XT, 1, 4, false, GROUPED>(a, s);
@@ -1236,6 +1248,9 @@ void launch_no_k(const MxArgs& a, hipStream_t s) {
 }
 
 template <bool GROUPED> int run_product(MxArgs& a, int x_type, void* stream) {
+  const MxPlan p = plan_product(a.M, a.N, a.x_rows > 0 ? a.K : 0, GROUPED ? a.E : 0, x_type);
+  if (!p.fits) return QG_E_UNSUPPORTED;
+  a.step = p.step;
   int st = device_present();
   if (st != QG_OK) return st;
   const void* ptrs[9] = {a.x, a.xs, a.w, a.ws, a.rows, a.offsets, a.row_scale, a.resid, a.y};
@@ -1247,8 +1262,6 @@ template <bool GROUPED> int run_product(MxArgs& a, int x_type, void* stream) {
     launch_no_k(a, s);
     return launch_status();
   }
-  const MxPlan p = plan_product(a.M, a.N, a.x_rows > 0 ? a.K : 0, GROUPED ? a.E : 0, x_type);
-  a.step = p.step;
   if (x_type == FP4) st = launch_product<FP4, GROUPED>(a, p, s);
   else if (x_type == BF16) st = launch_product<BF16, GROUPED>(a, p, s);
   else st = launch_product<F16, GROUPED>(a, p, s);

@@ -366,8 +366,8 @@ int qmx_dequantize(const uint8_t* codes, const uint8_t* scales, int M, int K, vo
  *   y        [device, out] y_type QG_MX_F16, QG_MX_BF16 or QG_MX_F32, leading dimension ldy >= N.
  * M == 0 or N == 0 is a no-op; K == 0 writes zeros (plus the residual).
  * Sums are added in a fixed order: equal inputs give equal bits.
- * Errors: QG_E_ARG, QG_E_ALIGN, QG_E_UNSUPPORTED (more pieces of y than a grid holds: beyond a
- * million rows of 16, 64 x 64 pieces beyond 2^31), QG_E_DEVICE, QG_E_NOT_DEVICE.
+ * Errors: QG_E_ARG, QG_E_ALIGN, QG_E_UNSUPPORTED (M or N beyond 2^31 - 513; more pieces of y than a
+ * grid holds: 2^24 of 64 x 64, 2^23 of the largest of qmx_plan), QG_E_DEVICE, QG_E_NOT_DEVICE.
  */
 int qmx_gemm(const void* x, int ldx, int x_type, const uint8_t* x_scales, const uint8_t* w,
              const uint8_t* w_scales, const void* residual, int ldr, int M, int N, int K, void* y, int ldy,
@@ -388,7 +388,7 @@ int qmx_gemm(const void* x, int ldx, int x_type, const uint8_t* x_scales, const 
  *             the arrays; where they decrease or leave [0, T], what y's rows then hold is unspecified.
  *   row_scale [device, in] fp32 [T], multiplied in fp32 before the rounding, or NULL.
  *   y         [device, out] [T, N].  Rows outside [offsets[0], offsets[E]) are left as they were.
- * Errors as qmx_gemm (QG_E_UNSUPPORTED for E > 65535 too).
+ * Errors as qmx_gemm (QG_E_UNSUPPORTED for E > 65535 too, and without a k for N beyond 2^30 - 16).
  */
 int qmx_gemm_grouped(const void* x, int ldx, int x_type, const uint8_t* x_scales, int x_rows,
                      const int32_t* rows, const uint8_t* w, const uint8_t* w_scales, const int32_t* offsets,
@@ -402,8 +402,9 @@ int qmx_gemm_grouped(const void* x, int ldx, int x_type, const uint8_t* x_scales
  * 64 x 128, 128 x 128 or 256 x 256 (16-bit x: 128 x 256) outputs; out[1],
  * out[2] = column blocks of 16 and waves a workgroup of the former; out[3] =
  * pieces of y (an estimate where grouped).  QMX_TILE=0..4 in the environment
- * forces out[0].  K == 0 without groups has an elementwise kernel of its own and is told as 0.  M == 0 or N == 0: all zero but out[1] and out[2], which are 1.
- * Errors: QG_E_ARG, QG_E_UNSUPPORTED (M, N or E beyond what the products take). */
+ * forces out[0].  K == 0 without groups has an elementwise kernel of its own
+ * and is told as 0.  M == 0 or N == 0: all zero but out[1] and out[2], 1 each.
+ * Errors: QG_E_ARG, QG_E_UNSUPPORTED (M or N beyond 2^31 - 513, E beyond 65535). */
 int qmx_plan(int M, int N, int K, int E, int x_type, int out[4]);
 
 /*

@@ -492,6 +492,26 @@ def test_gemm_without_k_of_any_size(kind, yt, M, N):
     assert torch.equal(out[:M, :N], r)
 
 
+def test_gemm_a_billion_rows():
+    # offsets far past 32 bits, and more 64 x 64 tiles than the 2^32 - 1 lanes of a grid: larger ones are taken
+    M, N, K = (1 << 30) + 70, 16, 32
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    rng = np.random.default_rng(0)
+    x, xs = torch.zeros(M, K // 2, dtype=torch.uint8, device=DEV), torch.full((M, 1), 127, dtype=torch.uint8, device=DEV)
+    few, fews, xv = make_x(rng, "mx", 6, K)
+    at = torch.tensor([0, 1, 1 << 29, (1 << 30) - 1, M - 70, M - 1], device=DEV)
+    x[at], xs[at] = few, fews
+    wc, wsc = random_mx(rng, N, K)
+    out = torch.full((M + 1, N), 9.0, dtype=F16, device=DEV)
+    qgm.mx_gemm(x, dev(wc), dev(wsc), x_scales=xs, out=out[:M])
+    ref, mag = mxref.mx_gemm_ref(xv, mxref.mx_values(wc, wsc))
+    check(out[at], ref, mag, K)
+    assert bool((out[M] == 9).all())
+    out[at] = 0
+    assert not any(bool(out[i:i + (1 << 27)].any()) for i in range(0, M - 70, 1 << 27)) and not bool(out[M - 70:M].any())
+
+
 # -------------------------------------------- as used together, graphs, streams
 
 def moe(x, up, down, offsets, rows, scale):

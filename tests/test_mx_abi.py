@@ -138,6 +138,32 @@ def test_grouped_refuses(kw, expect):
     assert grouped(**kw) == expect
 
 
+@pytest.mark.parametrize("tile,call", [
+    (None, lambda: gemm(xt=BF16, M=1 << 30, N=16, K=32)), (None, lambda: gemm(xt=F16, M=(1 << 31) - 600, N=4, K=64)),
+    (0, lambda: gemm(M=65535 * 16 + 1)), (1, lambda: gemm(xt=FP4, xs=A, M=1 << 30)),
+    (1, lambda: gemm(M=1 << 18, N=1 << 18)), (4, lambda: gemm(xt=BF16, M=1 << 19, N=1 << 19)),
+    (4, lambda: gemm(xt=FP4, xs=A, M=1 << 20, N=1 << 19)), (2, lambda: grouped(T=1 << 30, E=5)),
+    (None, lambda: grouped(xt=BF16, T=(1 << 30) + 7, xr=1 << 30, E=1)), (None, lambda: grouped(K=0, N=1 << 30)),
+    (None, lambda: grouped(xr=0, x=None, N=(1 << 30) - 15)), (None, lambda: gemm(M=(1 << 31) - 1)),
+    (None, lambda: gemm(N=(1 << 31) - 512)), (None, lambda: grouped(T=(1 << 31) - 100))])
+def test_more_than_a_grid_holds(monkeypatch, tile, call):
+    if tile is not None:
+        monkeypatch.setenv("QMX_TILE", str(tile))
+    assert call() == E_UNSUP
+
+
+@pytest.mark.skipif(gpu_present(), reason="checks the no-device status; a GPU is present")
+@pytest.mark.parametrize("tile,call", [
+    (None, lambda: gemm(xt=FP4, xs=A, M=(1 << 30) + 70, N=16, K=32)), (None, lambda: gemm(M=1 << 22, K=0)),
+    (0, lambda: gemm(M=65535 * 16)), (1, lambda: gemm(M=(1 << 18) - 64, N=1 << 18)),
+    (4, lambda: gemm(xt=FP4, xs=A, M=(1 << 20) - 256, N=1 << 19)), (None, lambda: grouped(K=0, N=(1 << 30) - 16)),
+    (None, lambda: gemm(M=(1 << 31) - 600, K=0))])
+def test_what_a_grid_holds_comes_to_the_device(monkeypatch, tile, call):
+    if tile is not None:
+        monkeypatch.setenv("QMX_TILE", str(tile))
+    assert call() == E_DEVICE
+
+
 @pytest.mark.skipif(gpu_present(), reason="checks the no-device status; a GPU is present")
 def test_no_device_status():
     assert quantize() == E_DEVICE and dequantize() == E_DEVICE
