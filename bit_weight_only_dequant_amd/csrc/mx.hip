@@ -437,7 +437,7 @@ __global__ __launch_bounds__(NW * 64) void mx_rows_kernel(MxArgs a) {
     W w0, w1;
     int nb = blockIdx.x, turn = 0, buf = 0;
     if (chunks > 0) load_w(nb, min(wave, chunks - 1), w0);
-    const bool has = xr >= 0 && xr < a.x_rows;
+    const bool has = !GROUPED || (xr >= 0 && xr < a.x_rows);
     xr = has ? xr : 0;
     // x: a whole chunk of the rows there are (past K: a row's last piece again)
     auto load_x = [&](int c) {
@@ -1194,33 +1194,31 @@ int device_present() {
   return st;
 }
 
-template <int XT, int NT, int NW, bool SHORT, bool GROUPED> int launch_rows(const MxArgs& a, hipStream_t s) {
+template <int XT, int NT, int NW, bool SHORT, bool GROUPED> void launch_rows(const MxArgs& a, hipStream_t s) {
   const int64_t gy = GROUPED ? a.E : ((int64_t)a.M + 15) / 16;
   const size_t lds = (size_t)NW * rows_x_bytes<XT>(a.M, a.step) + 2 * NW * NT * 1024;
-  if constexpr (NW > 4) {
-    if (lds > 160 * 1024) return launch_rows<XT, NT, NW / 2, SHORT, GROUPED>(a, s);
-  }
   // column blocks a workgroup takes: no more workgroups than keep 32 waves on every CU.  A grouped product
   // without a k to go through takes one (the kernel for several sends for the next block's weights).
   const int64_t blocks = (a.N + 16 * NT - 1) / (16 * NT), active = GROUPED ? std::min(a.E, a.M) : gy;
   const bool none = GROUPED && SHORT && (a.K == 0 || a.x_rows == 0);
   const int64_t slots = 256 * 32 / NW, share = none ? 1 : (blocks * active + slots - 1) / slots;
   const dim3 grid((unsigned)((blocks + share - 1) / share), (unsigned)gy);
-  if (none || (share == 1 && a.K <= 512 * NW))
-    hipLaunchKernelGGL((mx_rows_kernel<XT, NT, NW, SHORT, false, GROUPED>), grid, dim3(NW * 64), lds, s, a);
-  else
-    hipLaunchKernelGGL((mx_rows_kernel<XT, NT, NW, SHORT, true, GROUPED>), grid, dim3(NW * 64), lds, s, a);
-  return QG_OK;
+  if constexpr (NT == 1) {   // two blocks are for a K of several chunks a wave
+    if (none || (share == 1 && a.K <= 512 * NW)) {
+      hipLaunchKernelGGL((mx_rows_kernel<XT, NT, NW, SHORT, false, GROUPED>), grid, dim3(NW * 64), lds, s, a);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((mx_rows_kernel<XT, NT, NW, SHORT, true, GROUPED>), grid, dim3(NW * 64), lds, s, a);
 }
 
-template <int XT, int MI, int NI, int WM, int WN, int RING, bool GROUPED> int launch_tiles(const MxArgs& a, hipStream_t s) {
+template <int XT, int MI, int NI, int WM, int WN, int RING, bool GROUPED> void launch_tiles(const MxArgs& a, hipStream_t s) {
   constexpr int TM = 32 * MI * WM, TN = 32 * NI * WN;
   const dim3 grid((unsigned)tile_grid(a.M, a.N, GROUPED ? a.E : 0, TM, TN));
   hipLaunchKernelGGL((mx_tile_kernel<XT, MI, NI, WM, WN, RING, GROUPED>), grid, dim3(WM * WN * 64), 0, s, a, (a.N + TN - 1) / TN);
-  return QG_OK;
 }
 
-template <int XT, bool GROUPED> int launch_product(const MxArgs& a, const MxPlan& p, hipStream_t s) {
+template <int XT, bool GROUPED> void launch_product(const MxArgs& a, const MxPlan& p, hipStream_t s) {
   if constexpr (XT == FP4) {
     if (p.tile == 4) return launch_tiles<XT, 4, 2, 2, 4, 4, GROUPED>(a, s);
     if (p.tile == 3) return launch_tiles<XT, 2, 2, 2, 2, 4, GROUPED>(a, s);
@@ -1233,7 +1231,9 @@ template <int XT, bool GROUPED> int launch_product(const MxArgs& a, const MxPlan
     if (p.tile == 1) return launch_tiles<XT, 1, 1, 2, 2, 3, GROUPED>(a, s);
   }
   if (a.K < 512 || a.x_rows == 0) return launch_rows<XT, 1, 1, true, GROUPED>(a, s);
-  if (p.nt == 2) return launch_rows<XT, 2, 8, false, GROUPED>(a, s);
+  if constexpr (XT != FP4) {   // 16 rows of MXFP4 x fit into LDS for 16 waves
+    if (p.nt == 2) return launch_rows<XT, 2, 8, false, GROUPED>(a, s);
+  }
   if (p.nw == 2) return launch_rows<XT, 1, 2, false, GROUPED>(a, s);
   if (p.nw == 4) return launch_rows<XT, 1, 4, false, GROUPED>(a, s);
   if (p.nw == 8) return launch_rows<XT, 1, 8, false, GROUPED>(a, s);
@@ -1262,10 +1262,10 @@ template <bool GROUPED> int run_product(MxArgs& a, int x_type, void* stream) {
     launch_no_k(a, s);
     return launch_status();
   }
-  if (x_type == FP4) st = launch_product<FP4, GROUPED>(a, p, s);
-  else if (x_type == BF16) st = launch_product<BF16, GROUPED>(a, p, s);
-  else st = launch_product<F16, GROUPED>(a, p, s);
-  return st != QG_OK ? st : launch_status();
+  if (x_type == FP4) launch_product<FP4, GROUPED>(a, p, s);
+  else if (x_type == BF16) launch_product<BF16, GROUPED>(a, p, s);
+  else launch_product<F16, GROUPED>(a, p, s);
+  return launch_status();
 }
 
 // Checks shared by the two products; fills the fields that both use.
