@@ -512,6 +512,48 @@ def test_gemm_a_billion_rows():
     assert not any(bool(out[i:i + (1 << 27)].any()) for i in range(0, M - 70, 1 << 27)) and not bool(out[M - 70:M].any())
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(9, 8192, 4128), (12, 8195, 4608), (16, 8200, 8192), (16, 8193, 9248)])
+def test_gemm_two_column_blocks(monkeypatch, kind, M, N, K):
+    # 9 to 16 rows against many columns of a long K: two column blocks share a reading of x.  Columns that
+    # end inside the first block of a pair, inside the second and with it; K that ends inside a chunk
+    monkeypatch.setenv("QMX_TILE", "0")
+    assert qgm.mx_plan(M, N, K, qgm.MX_F16)["blocks"] == 2
+    rng = np.random.default_rng(M + N + K)
+    wc, wsc = random_mx(rng, N, K, spread=0)
+    w, wv = dev(wc), mxref.mx_values(wc, wsc)
+    x, _, xv = make_x(rng, kind, M, K, exact=True)
+    out = torch.full((M + 1, N), 9.0, dtype=F32, device=DEV)
+    qgm.mx_gemm(x, w, dev(wsc), out=out[:M])
+    assert np.array_equal(f64(out[:M]), mxref.mx_gemm_ref(xv, wv)[0])
+    assert bool((out[M] == 9).all())
+    # every size of scale, also past fp16's; a residual
+    wsc = rng.integers(95, 150, wsc.shape).astype(np.uint8)
+    x, _, xv = make_x(rng, kind, M, K)
+    r = torch.randn(M, N, dtype=F32)
+    ref, mag = mxref.mx_gemm_ref(xv, mxref.mx_values(wc, wsc), residual=f64(r))
+    check(qgm.mx_gemm(x, w, dev(wsc), out_dtype=F32, residual=r.to(DEV)), ref, mag, K)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("sizes", [[10, 0, 9, 21], [33, 1, 0, 6]])
+def test_grouped_two_column_blocks(monkeypatch, kind, sizes):
+    monkeypatch.setenv("QMX_TILE", "0")
+    rng = np.random.default_rng(sizes[0])
+    E, N, K = len(sizes), 4100, 8192
+    off, T = make_groups(sizes), sum(sizes)
+    assert qgm.mx_plan(T, N, K, qgm.MX_F16, groups=E)["blocks"] == 2
+    rows, scale = rng.integers(-1, 13, T).astype(np.int32), rng.standard_normal(T).astype(np.float32)
+    x, _, xv = make_x(rng, kind, 12, K)
+    wc, wsc = random_mx(rng, E * N, K)
+    out = torch.full((T + 1, N), 9.0, dtype=F32, device=DEV)
+    qgm.mx_gemm_grouped(x, dev(wc).view(E, N, -1), dev(wsc).view(E, N, -1), dev(off), rows=dev(rows),
+                        row_scale=dev(scale), out=out[:T])
+    ref, mag = mxref.mx_grouped_ref(xv, mxref.mx_values(wc, wsc).reshape(E, N, K), off, rows, scale)
+    check(out[:T], ref, mag, K)
+    assert bool((out[T] == 9).all())
+
+
 # -------------------------------------------- as used together, graphs, streams
 
 def moe(x, up, down, offsets, rows, scale):
