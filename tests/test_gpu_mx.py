@@ -554,6 +554,33 @@ def test_grouped_two_column_blocks(monkeypatch, kind, sizes):
     assert bool((out[T] == 9).all())
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16", "mx"])
+@pytest.mark.parametrize("sizes", [[0] * 15 + [23] + [0] * 4, [9, 0, 17] + [0] * 20, [0, 64] + [0] * 30, [8, 16, 1] + [0] * 12],
+                         ids=lambda s: "-".join(map(str, s[:4])))
+@pytest.mark.parametrize("N,K", [(50, 416), (50, 1024), (1030, 4128), (70, 9248)])
+def test_grouped_skewed_router(monkeypatch, kind, sizes, N, K):
+    # few slots a matrix on average, most of them one expert's: its rows go eight (16-bit x) at a time through
+    # the same workgroup, with K below a chunk, one chunk a wave and several
+    monkeypatch.setenv("QMX_TILE", "0")
+    rng = np.random.default_rng(sum(sizes) + K)
+    E, off, T, xr = len(sizes), make_groups(sizes), sum(sizes), 11
+    assert T <= 2 * E
+    rows, scale = rng.integers(-1, xr, T).astype(np.int32), rng.standard_normal(T).astype(np.float32)
+    x, xs, xv = make_x(rng, kind, xr, K)
+    used = [e for e in range(E) if sizes[e]]
+    wc, wsc = np.zeros((E, N, K // 2), dtype=np.uint8), np.full((E, N, K // 32), 255, dtype=np.uint8)   # others: NaN
+    for e in used:
+        wc[e], wsc[e] = random_mx(rng, N, K)
+    wv = np.zeros((E, N, K))
+    for e in used:
+        wv[e] = mxref.mx_values(wc[e], wsc[e])
+    out = torch.full((T + 1, N), 9.0, dtype=F32, device=DEV)
+    qgm.mx_gemm_grouped(x, dev(wc), dev(wsc), dev(off), x_scales=xs, rows=dev(rows), row_scale=dev(scale), out=out[:T])
+    ref, mag = mxref.mx_grouped_ref(xv, wv, off, rows, scale)
+    check(out[:T], ref, mag, K)
+    assert bool((out[T] == 9).all())
+
+
 # -------------------------------------------- as used together, graphs, streams
 
 def moe(x, up, down, offsets, rows, scale):
