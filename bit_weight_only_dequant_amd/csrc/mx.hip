@@ -1087,8 +1087,11 @@ int check_matrix(const void* v, int ld, int type, int M, int K, const void* code
   return QG_OK;
 }
 
-// Grid of an elementwise kernel over rows x n8 groups: enough workgroups to
-// fill the chip eight times over, the rest by the kernel's own loops.
+// Grid of an elementwise kernel over rows x n8 groups: as many workgroups along
+// a row as fill the chip's wave slots twice (16 a CU, of 4 waves), the rest by
+// the kernel's own loops.  A matrix whose rows follow each other is one row
+// here; strided rows narrower than a workgroup's 256 groups leave lanes idle
+// (K = 32: 4 of 256 work).
 dim3 ew_grid(int64_t rows, int64_t n8) {
   const int64_t bx = std::min<int64_t>((n8 + EW_THREADS - 1) / EW_THREADS, 256 * 16);
   return dim3((unsigned)std::max<int64_t>(bx, 1), (unsigned)std::min<int64_t>(rows, 65535));
