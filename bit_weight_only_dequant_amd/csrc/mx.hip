@@ -11,13 +11,15 @@
 //   mx_rows              few rows.  W and its scales go from memory straight to
 //                        the matrix instruction's registers in their stored
 //                        order, x through LDS; waves split K.  1 x 6144 x 2048
-//                        with fp16 x 5.2 us, 8 x 2048 x 8192 with bf16 x 7.2 to
-//                        8.0 us, 1 x 8192 x 8192 with bf16 x 10.0 us (3.6 TB/s),
-//                        each in a replayed graph.
+//                        with fp16 x 4.8 us, 8 x 2048 x 8192 with bf16 x 7.1 to
+//                        7.7 us, 1 x 8192 x 8192 with bf16 x 10.1 us (3.5 TB/s),
+//                        each in a replayed graph with the operands in the
+//                        on-die cache; evicted 5.7, 8.1 to 8.4 and 10.8 us.
 //   mx_tile              more rows.  x and W through a ring of LDS stages by
-//                        direct loads.  MXFP4 x: 4096 x 8192 x 8192 142 to 152
-//                        us (3.6 to 3.9 PFLOP/s); bf16 x: 2048 x 8192 x 8192 224
-//                        us (1.23 PFLOP/s; the library's bf16 product reaches 1.37).
+//                        direct loads.  MXFP4 x: 4096 x 8192 x 8192 138 to 142 us
+//                        (3.9 PFLOP/s), evicted 157 to 166; bf16 x: 2048 x 8192 x
+//                        8192 216 us (1.27 PFLOP/s; the library's bf16 product
+//                        reaches 1.39), evicted 249.
 //   mx_no_k              a product without a k: the residual, or zeros.
 // The stored form needs no packing step: 16 consecutive bytes of a row are one
 // block of 32, which is what one lane supplies to v_mfma_scale_f32_16x16x128 and
