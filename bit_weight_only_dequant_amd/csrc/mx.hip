@@ -754,8 +754,9 @@ __global__ __launch_bounds__(WM * WN * 64) void mx_tile_kernel(MxArgs a, int til
 
   if constexpr (GROUPED) {
     for (int i = tid; i < t.m_end - t.m0; i += NW * 64) {
+      const float factor = a.row_scale ? a.row_scale[t.m0 + i] : 1.f;   // loaded beside the row's number
       const bool has = has_row<true>(a, t.m0 + i);   // without a row: zero whatever the slot's factor holds
-      info[i] = f2{a.row_scale && has ? a.row_scale[t.m0 + i] : 1.f, has ? 1.f : 0.f};
+      info[i] = f2{has ? factor : 1.f, has ? 1.f : 0.f};
     }
   }
   // direct loads: lane l brings a 16-byte chunk of row l / 4 of 16 (16-bit x: row l / 16 of 4)
