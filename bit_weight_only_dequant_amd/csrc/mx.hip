@@ -34,38 +34,17 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <atomic>
 #include <climits>
 #include <type_traits>
 
 #include "../../include/qgemm.h"
+#include "device.h"
 #include "internal.h"
 
 namespace qg {
 namespace {
 
-typedef _Float16 f16;
-typedef __bf16 bf16;
-typedef f16 h2 __attribute__((ext_vector_type(2)));
-typedef f16 h8 __attribute__((ext_vector_type(8)));
-typedef bf16 b2 __attribute__((ext_vector_type(2)));
-typedef bf16 b8 __attribute__((ext_vector_type(8)));
-typedef float f2 __attribute__((ext_vector_type(2)));
-typedef float f4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-typedef int i8v __attribute__((ext_vector_type(8)));
-typedef float f16v __attribute__((ext_vector_type(16)));
-
-constexpr int F16 = QG_MX_F16, BF16 = QG_MX_BF16, F32 = QG_MX_F32, FP4 = QG_MX_FP4;
-
-template <int T> struct Elem;
-template <> struct Elem<F16> { typedef f16 type; };
-template <> struct Elem<BF16> { typedef bf16 type; };
-template <> struct Elem<F32> { typedef float type; };
-
-__device__ __forceinline__ float bits_f32(uint32_t v) { return __builtin_bit_cast(float, v); }
-__device__ __forceinline__ uint32_t f32_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
+constexpr int FP4 = QG_MX_FP4;
 
 // The E8M0 byte s as the conversions take their scale: the exponent field of
 // an fp32 number (field 0 is 2^-127 there, 255 NaN).
@@ -79,36 +58,6 @@ __device__ __forceinline__ float scale_f32(uint32_t s) { return bits_f32(s << 23
 // find its largest magnitude with two quad permutes; a wave's codes are 256
 // contiguous bytes.  The maximum is taken over the bit patterns without the
 // sign, which order like the magnitudes and put infinities and NaN on top.
-constexpr int EW_THREADS = 256;
-
-template <int T> __device__ __forceinline__ void load8(const void* p, float v[8]) {
-  if constexpr (T == F32) {
-    const f4 a = reinterpret_cast<const f4*>(p)[0], b = reinterpret_cast<const f4*>(p)[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[i + 4] = b[i];
-    }
-  } else if constexpr (T == BF16) {
-    const u4 a = *reinterpret_cast<const u4*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bits_f32(a[i] << 16);
-      v[2 * i + 1] = bits_f32(a[i] & 0xffff0000u);
-    }
-  } else {
-    const h8 a = *reinterpret_cast<const h8*>(p);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)a[i];
-  }
-}
-
-// largest of the four lanes of a quad (quad_perm 1,0,3,2 then 2,3,0,1)
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xf, 0xf, true));
-  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xf, 0xf, true));
-}
-
 // Rows of n8 groups of 8 elements (a contiguous matrix is one long row).
 // The four lanes of a block are active together: n8 is a multiple of 4.
 template <int T>
@@ -246,61 +195,6 @@ template <int S> __device__ __forceinline__ f16v mfma_fp4_32(u4 a, uint32_t sa, 
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, S, (int)sa, S, (int)sb);
 }
 
-// C 16- or 32-bit values at element alignment, in vectors of up to 16 bytes
-template <int C, typename E> __device__ __forceinline__ void get(const E* p, E (&v)[C]) {
-  constexpr int B = C * sizeof(E) >= 16 ? 16 : 8;
-  typedef uint32_t vec __attribute__((ext_vector_type(B / 4), aligned(2)));
-#pragma unroll
-  for (int i = 0; i < (int)(C * sizeof(E)) / B; ++i) {
-    const vec t = reinterpret_cast<const vec*>(p)[i];
-    __builtin_memcpy(reinterpret_cast<char*>(v) + i * B, &t, B);
-  }
-}
-template <int C, typename E> __device__ __forceinline__ void put(E* p, const E (&v)[C]) {
-  constexpr int B = C * sizeof(E) >= 16 ? 16 : 8;
-  typedef uint32_t vec __attribute__((ext_vector_type(B / 4), aligned(2)));
-#pragma unroll
-  for (int i = 0; i < (int)(C * sizeof(E)) / B; ++i) {
-    vec t;
-    __builtin_memcpy(&t, reinterpret_cast<const char*>(v) + i * B, B);
-    reinterpret_cast<vec*>(p)[i] = t;
-  }
-}
-
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(f16 v) { return (float)v; }
-__device__ __forceinline__ float to_f32(bf16 v) { return bits_f32((uint32_t)__builtin_bit_cast(uint16_t, v) << 16); }
-
-// C (4 or 8) consecutive outputs of one row, columns n .. n+C-1 of row m: the
-// factor and the residual in fp32, one rounding.  Rows of any pitch are stored
-// in one piece (the device takes vector accesses at element alignment).
-template <int YT, int C> __device__ __forceinline__ void store_cols_as(const MxArgs& a, int m, int n, float (&v)[C], float factor) {
-  typedef typename Elem<YT>::type E;
-  const bool whole = n + C <= a.N;
-  const int have = min(a.N - n, C);
-#pragma unroll
-  for (int i = 0; i < C; ++i) v[i] *= factor;
-  if (a.resid) {
-    E r[C] = {};
-    const E* rp = reinterpret_cast<const E*>(a.resid) + (int64_t)m * a.ldr + n;
-    if (whole) get(rp, r);
-    else for (int i = 0; i < C; ++i) if (i < have) r[i] = rp[i];
-#pragma unroll
-    for (int i = 0; i < C; ++i) v[i] += to_f32(r[i]);
-  }
-  E q[C];
-#pragma unroll
-  for (int i = 0; i < C; ++i) q[i] = (E)v[i];
-  E* y = reinterpret_cast<E*>(a.y) + (int64_t)m * a.ldy + n;
-  if (whole) put(y, q);
-  else for (int i = 0; i < C; ++i) if (i < have) y[i] = q[i];
-}
-template <int C> __device__ __forceinline__ void store_cols(const MxArgs& a, int m, int n, float (&v)[C], float factor) {
-  if (a.y_type == F32) store_cols_as<F32, C>(a, m, n, v, factor);
-  else if (a.y_type == F16) store_cols_as<F16, C>(a, m, n, v, factor);
-  else store_cols_as<BF16, C>(a, m, n, v, factor);
-}
-
 // A grouped product's slots of expert e, kept within [0, T] whatever the
 // offsets hold.
 __device__ __forceinline__ void group_bounds(const MxArgs& a, int e, int& begin, int& end) {
@@ -323,15 +217,6 @@ template <bool GROUPED> __device__ __forceinline__ bool has_row(const MxArgs& a,
   return m >= 0 && m < a.x_rows;
 }
 
-typedef const void __attribute__((address_space(1)))* gptr;
-typedef void __attribute__((address_space(3)))* lptr;
-
-// At most N of this wave's global loads are on their way, and none of its LDS
-// reads (s_waitcnt vmcnt(N) lgkmcnt(0), GFX9 encoding).
-template <int N> __device__ __forceinline__ void wait_loads() {
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
-}
-
 // Few rows: bound by the weights' bytes, and next to them by the number of
 // vector loads (one takes a CU's address unit about 16 cycles however little it
 // brings).  A workgroup owns 16*NT columns of y (rows of W) and up to 16 rows
@@ -347,17 +232,6 @@ template <int N> __device__ __forceinline__ void wait_loads() {
 // while one is multiplied and summed; where every wave has one chunk, x stays.
 // W is the first operand, so a lane ends with four consecutive outputs of one
 // row.
-
-// All of this wave's LDS reads have arrived (s_waitcnt lgkmcnt(0)).
-__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }
-
-// A barrier that waits for LDS accesses only: loads stay on their way.
-__device__ __forceinline__ void lds_barrier() {
-  wait_lds();
-  asm volatile("" ::: "memory");        // no LDS access moves across the barrier
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
 
 // LDS of a wave for a chunk of x: whole direct loads of a kilobyte (four MXFP4 rows, one 16-bit row)
 template <int XT> __host__ __device__ constexpr int rows_x_bytes(int M, int step) {
@@ -1079,25 +953,12 @@ template <int YT> __global__ __launch_bounds__(EW_THREADS) void mx_no_k_kernel(M
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-bool float_type(int t) { return t == F16 || t == BF16 || t == F32; }
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 int check_matrix(const void* v, int ld, int type, int M, int K, const void* codes, const void* scales) {
   if (!float_type(type) || M < 0 || K < 0 || K % 32) return QG_E_ARG;
   if (M == 0 || K == 0) return QG_OK;
   if (!v || !codes || !scales || ld < K) return QG_E_ARG;
   if (!aligned(v, 16) || !aligned(codes, 16) || ld % 8) return QG_E_ALIGN;
   return QG_OK;
-}
-
-// Grid of an elementwise kernel over rows x n8 groups: as many workgroups along
-// a row as fill the chip's wave slots twice (16 a CU, of 4 waves), the rest by
-// the kernel's own loops.  A matrix whose rows follow each other is one row
-// here; strided rows narrower than a workgroup's 256 groups leave lanes idle
-// (K = 32: 4 of 256 work).
-dim3 ew_grid(int64_t rows, int64_t n8) {
-  const int64_t bx = std::min<int64_t>((n8 + EW_THREADS - 1) / EW_THREADS, 256 * 16);
-  return dim3((unsigned)std::max<int64_t>(bx, 1), (unsigned)std::min<int64_t>(rows, 65535));
 }
 
 // Which kernel takes a product.  tile 0: mx_rows_kernel with nt column blocks
@@ -1185,19 +1046,6 @@ MxPlan plan_product(int M, int N, int K, int E, int x_type) {
     p.workgroups = row_tiles(16) * (((int64_t)N + 16 * p.nt - 1) / (16 * p.nt));
   }
   return p;
-}
-
-int launch_status() { return hip_status(hipGetLastError()); }
-
-// QG_OK when there is a device to launch on.  Asking takes the runtime about a
-// microsecond; once one was there it is not asked again.
-int device_present() {
-  static std::atomic<bool> seen{false};
-  if (seen.load(std::memory_order_relaxed)) return QG_OK;
-  int dev = 0;
-  const int st = current_device(&dev);
-  if (st == QG_OK) seen.store(true, std::memory_order_relaxed);
-  return st;
 }
 
 template <int XT, int NT, int NW, bool SHORT, bool GROUPED> void launch_rows(const MxArgs& a, hipStream_t s) {
