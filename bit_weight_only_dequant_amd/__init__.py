@@ -65,6 +65,10 @@ _SIGS = {
     "qmx_gemm": ([_P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P], _I),
     "qmx_gemm_grouped": ([_P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _I, _I, _P, _I, _I, _P], _I),
     "qmx_plan": ([_I, _I, _I, _I, _I, ctypes.POINTER(_I)], _I),
+    "qf8_quantize": ([_P, _I, _I, _I, _I, _I, _I, _P, _P, _P], _I),
+    "qf8_gemm": ([_P, _I, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _P, _I, _I, _P], _I),
+    "qf8_gated": ([_P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P], _I),
+    "qf8_gated_grad": ([_P, _I, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P], _I),
     "qg_stream_read": ([_P, _SZ, _P, _I, _P], _I),
     "qg_empty_launch": ([_I, _I, _P], _I),
     "qg_mfma_probe": ([_P, _I, _I, _P], _I),
@@ -680,6 +684,216 @@ class MXLinear:
     def __call__(self, x, x_scales=None, out=None, out_dtype=None, residual=None, stream=None):
         return mx_gemm(x, self.codes, self.scales, x_scales=x_scales, out=out, out_dtype=out_dtype,
                        residual=residual, stream=stream)
+
+
+# ----------------------------------------------------------------------------
+# 8-bit floating point (E4M3) with an fp32 scale for blocks of 128: codes
+# torch.float8_e4m3fn [R, K] and scales fp32 [R, ceil(K/128)] (block 1) or
+# [ceil(R/128), ceil(K/128)] (block 128), both contiguous, K a multiple of 16;
+# see include/qgemm.h.
+
+F8_E4M3 = 4
+F8_BLOCK = 128
+F8_ACTS = {"silu": 0, "gelu_tanh": 1}
+_CODE = torch.float8_e4m3fn
+
+
+def _f8_blocks(n):
+    return (n + F8_BLOCK - 1) // F8_BLOCK
+
+
+def _f8_matrix(codes, scales, what, dev, block=None):
+    """(R, K, block) of a matrix of codes and scales; block: the one it must have."""
+    sh = codes.shape
+    if (codes.dtype is _CODE and scales.dtype is _F32 and len(sh) == 2 and sh[1] % 16 == 0
+            and codes.get_device() == dev and scales.get_device() == dev
+            and codes.is_contiguous() and scales.is_contiguous()):
+        R, K = sh
+        kb = _f8_blocks(K)
+        if (R | K) >> 31:
+            _mx_int(what, R, K)
+        if block != 1 and scales.shape == (_f8_blocks(R), kb):
+            return R, K, 128
+        if block != 128 and scales.shape == (R, kb):
+            return R, K, 1
+    rows = {1: "R", 128: "ceil(R/128)", None: "R or ceil(R/128)"}[block]
+    raise ValueError(f"{what} must be contiguous {_CODE} codes [R, K], K a multiple of 16, and fp32 scales "
+                     f"[{rows}, ceil(K/128)] on GPU {dev}; got {codes.dtype} {list(sh)} on {codes.device} and "
+                     f"{scales.dtype} {list(scales.shape)} on {scales.device}")
+
+
+def _f8_x(x, x_scales, K, dev):
+    """(type, leading dimension, scales pointer) of a product's left operand."""
+    if x_scales is None:
+        xt, ldx = _mx_float(x, "x (without x_scales)", dev, None, _MX_X16)
+        if x.shape[1] != K:
+            raise ValueError(f"x must have {K} columns, as w has; got {x.shape[1]}")
+        return xt, ldx, None
+    if _f8_matrix(x, x_scales, "x and x_scales", dev, 1)[1] != K:
+        raise ValueError(f"x (codes) must have {K} columns, as w has; got {x.shape[1]}")
+    return F8_E4M3, K, x_scales.data_ptr()
+
+
+def _f8_act(act):
+    if act not in F8_ACTS:
+        raise ValueError(f"act must be one of {', '.join(F8_ACTS)}; got {act!r}")
+    return F8_ACTS[act]
+
+
+def _f8_gate_weights(w, w_scales, dev):
+    """(F, K) of the two projections' weights [2F, K]."""
+    R, K, _ = _f8_matrix(w, w_scales, "w and w_scales", dev, 128)
+    if R % 32:
+        raise ValueError(f"w must have 2F rows with F a multiple of 16; got {R}")
+    return R // 2, K
+
+
+def f8_quantize(x, block=1, transpose=False, codes=None, scales=None, stream=None):
+    """x [M, K] (fp16, bf16 or fp32, K a multiple of 16, unit column stride) ->
+    (codes, scales) in E4M3 with blocks of 128 elements of a row (block = 1) or
+    of 128 x 128 (block = 128).  transpose: those of x transposed, its rows
+    padded with zeros to a multiple of 16 columns; see qf8_quantize."""
+    ctx = _mx_elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return f8_quantize(x, block, transpose, codes, scales)
+    dev = x.get_device()
+    xt, ldx = _mx_float(x, "x", dev)
+    M, K = x.shape
+    if K % 16:
+        raise ValueError(f"K = {K} is not a multiple of 16")
+    if block not in (1, 128):
+        raise ValueError(f"block must be 1 or 128; got {block!r}")
+    R, C = (K, (M + 15) // 16 * 16) if transpose else (M, K)
+    if codes is None:
+        codes = x.new_empty((R, C), dtype=_CODE)
+    if scales is None:
+        scales = x.new_empty((R if block == 1 else _f8_blocks(R), _f8_blocks(C)), dtype=_F32)
+    if _f8_matrix(codes, scales, "codes and scales", dev, block)[:2] != (R, C):
+        raise ValueError(f"codes must be [{R}, {C}]")
+    st = _lib.qf8_quantize(x.data_ptr(), ldx, xt, M, K, block, 1 if transpose else 0, codes.data_ptr(),
+                           scales.data_ptr(), _mx_stream(dev))
+    if st:
+        raise QGemmError(st, "qf8_quantize")
+    return codes, scales
+
+
+def f8_gemm(x, w, w_scales, x_scales=None, out=None, out_dtype=None, residual=None, stream=None):
+    """y = x . W^T (+ residual) with W [N, K] in E4M3 (codes w, scales w_scales).
+    x: fp16 or bf16 [M, K] with unit column stride, or E4M3 codes with x_scales
+    [M, ceil(K/128)]; w_scales in blocks of 128 x 128, or with 8-bit x [N,
+    ceil(K/128)] too.  y: out_dtype (fp16, bf16 or fp32; x's type by default,
+    fp16 for 8-bit x); see qf8_gemm."""
+    ctx = _mx_elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return f8_gemm(x, w, w_scales, x_scales, out, out_dtype, residual)
+    dev = x.get_device()
+    N, K, block = _f8_matrix(w, w_scales, "w and w_scales", dev, 128 if x_scales is None else None)
+    xt, ldx, xs = _f8_x(x, x_scales, K, dev)
+    M = x.shape[0]
+    y, yt, ldy = _mx_y(x, x_scales, out, out_dtype, M, N, dev)
+    rp, ldr = None, N
+    if residual is not None:
+        _, ldr = _mx_float(residual, "residual", dev, (M, N), {y.dtype: yt})
+        rp = residual.data_ptr()
+    st = _lib.qf8_gemm(x.data_ptr(), ldx, xt, xs, w.data_ptr(), w_scales.data_ptr(), block, rp, ldr, M, N, K,
+                       y.data_ptr(), ldy, yt, _mx_stream(dev))
+    if st:
+        raise QGemmError(st, "qf8_gemm")
+    return y
+
+
+def f8_gated(x, w, w_scales, x_scales=None, act="silu", out=None, out_dtype=None, stream=None):
+    """h = act(x . Wg^T) * (x . Wu^T) [M, F] in one kernel: w [2F, K] in E4M3 with
+    blocks of 128 x 128, Wg its first F rows and Wu the others (F a multiple of
+    16).  x and the result's type as f8_gemm; act: "silu" or "gelu_tanh"; see
+    qf8_gated."""
+    ctx = _mx_elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return f8_gated(x, w, w_scales, x_scales, act, out, out_dtype)
+    dev = x.get_device()
+    F, K = _f8_gate_weights(w, w_scales, dev)
+    at = _f8_act(act)
+    xt, ldx, xs = _f8_x(x, x_scales, K, dev)
+    M = x.shape[0]
+    h, ht, ldh = _mx_y(x, x_scales, out, out_dtype, M, F, dev)
+    st = _lib.qf8_gated(x.data_ptr(), ldx, xt, xs, w.data_ptr(), w_scales.data_ptr(), at, M, F, K, h.data_ptr(), ldh, ht,
+                        _mx_stream(dev))
+    if st:
+        raise QGemmError(st, "qf8_gated")
+    return h
+
+
+def f8_gated_grad(dh, x, w, w_scales, x_scales=None, act="silu", out=None, stream=None):
+    """The gradients of f8_gated's projections from dh [M, F] (fp16, bf16 or fp32,
+    unit column stride): d [M, 2F] of dh's type, dh * u * act'(g) beside dh *
+    act(g), with g and u computed again from x and w as f8_gated takes them.
+    The input's gradient is f8_gemm(d, w transposed); see qf8_gated_grad."""
+    ctx = _mx_elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return f8_gated_grad(dh, x, w, w_scales, x_scales, act, out)
+    dev = x.get_device()
+    F, K = _f8_gate_weights(w, w_scales, dev)
+    at = _f8_act(act)
+    xt, ldx, xs = _f8_x(x, x_scales, K, dev)
+    M = x.shape[0]
+    dt, lddh = _mx_float(dh, "dh", dev, (M, F))
+    if out is None:
+        out = dh.new_empty((M, 2 * F))
+    _, ldd = _mx_float(out, "out", dev, (M, 2 * F), {dh.dtype: dt})
+    st = _lib.qf8_gated_grad(dh.data_ptr(), lddh, x.data_ptr(), ldx, xt, xs, w.data_ptr(), w_scales.data_ptr(), at, M, F, K,
+                             out.data_ptr(), ldd, dt, _mx_stream(dev))
+    if st:
+        raise QGemmError(st, "qf8_gated_grad")
+    return out
+
+
+class F8Linear:
+    """One weight matrix [N, K] in E4M3 with blocks of 128 x 128 on the GPU: the
+    8-bit sibling of QuantLinear and MXLinear."""
+
+    def __init__(self, codes, scales):
+        _dev(codes, "codes")
+        self.N, self.K, _ = _f8_matrix(codes, scales, "codes and scales", codes.get_device(), 128)
+        self.codes, self.scales = codes, scales
+        self.weight_bytes = codes.numel() + 4 * scales.numel()
+
+    @classmethod
+    def from_weight(cls, weight, transpose=False, stream=None):
+        """Quantises weight [N, K] (fp16, bf16 or fp32 on the GPU), or its
+        transposed (the linear of the backward pass: the same values)."""
+        return cls(*f8_quantize(weight, block=128, transpose=transpose, stream=stream))
+
+    def __call__(self, x, x_scales=None, out=None, out_dtype=None, residual=None, stream=None):
+        return f8_gemm(x, self.codes, self.scales, x_scales=x_scales, out=out, out_dtype=out_dtype,
+                       residual=residual, stream=stream)
+
+
+class F8Gated:
+    """The gate and up projections [2F, K] of a feed-forward block in E4M3, with
+    its activation."""
+
+    def __init__(self, codes, scales, act="silu"):
+        _dev(codes, "codes")
+        _f8_act(act)
+        self.F, self.K = _f8_gate_weights(codes, scales, codes.get_device())
+        self.codes, self.scales, self.act = codes, scales, act
+        self.weight_bytes = codes.numel() + 4 * scales.numel()
+
+    @classmethod
+    def from_weight(cls, weight, act="silu", stream=None):
+        """Quantises weight [2F, K] (fp16, bf16 or fp32 on the GPU)."""
+        return cls(*f8_quantize(weight, block=128, stream=stream), act=act)
+
+    def __call__(self, x, x_scales=None, out=None, out_dtype=None, stream=None):
+        return f8_gated(x, self.codes, self.scales, x_scales=x_scales, act=self.act, out=out, out_dtype=out_dtype,
+                        stream=stream)
+
+    def grad(self, dh, x, x_scales=None, out=None, stream=None):
+        return f8_gated_grad(dh, x, self.codes, self.scales, x_scales=x_scales, act=self.act, out=out, stream=stream)
 
 
 # ----------------------------------------------------------------------------

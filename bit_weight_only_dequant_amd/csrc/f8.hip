@@ -1,0 +1,670 @@
+// f8.hip - 8-bit floating point (E4M3) with an fp32 scale for blocks of 128:
+// quantising, the product y = x . W^T, the two projections of a gated
+// feed-forward block with its activation, and that block's backward pass.
+// The format and the entry points are described in include/qgemm.h.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <climits>
+#include <type_traits>
+
+#include "../../include/qgemm.h"
+#include "device.h"
+#include "internal.h"
+
+namespace qg {
+namespace {
+
+constexpr int F8 = QG_F8_E4M3;
+constexpr float F8_TOP = 448.f;                 // the largest code
+constexpr float F8_LOWEST = 0x1p-100f;          // a block's largest magnitude counts as at least this
+
+// ---------------------------------------------------------------------------
+// quantise
+// ---------------------------------------------------------------------------
+// Bound by HBM.  A code is the nearest to q = 448 v / A, A the block's largest
+// magnitude, ties to the even one.  Quotients midway between two codes are
+// common, so q has to be exact there.  v and A are taken times the power of two
+// that makes A 1..2, so that nothing overflows; t is q rounded to 24 bits by
+// one step of division (a product with 448 / A, then its remainder times 1 / A).
+// Middles have at most 5 significant bits.  With 16-bit v the numerator 448 v
+// is exact in fp32, and a quotient that is not a middle is further from any
+// than t's rounding, so t decides.  With fp32 v the numerator takes two parts,
+// and where t is a middle the sign of what is left tells the side.
+struct F8Block { float inv, rcp, top; int shift; bool finite; };   // 448 / A, 1 / A, A, all at A's scale
+
+__device__ __forceinline__ F8Block f8_block(uint32_t top_bits) {   // the bits of A
+  F8Block b;
+  b.finite = top_bits < 0x7f800000u;
+  const uint32_t t = max(top_bits, f32_bits(F8_LOWEST));
+  b.shift = 127 - (int)(t >> 23);
+  b.top = bits_f32((t & 0x7fffffu) | 0x3f800000u);
+  b.inv = F8_TOP / b.top;
+  b.rcp = b.inv * (1.f / F8_TOP);
+  return b;
+}
+__device__ __forceinline__ float f8_scale(uint32_t top_bits) {
+  return top_bits < 0x7f800000u ? fmaxf(bits_f32(top_bits), F8_LOWEST) / F8_TOP : bits_f32(0x7fc00000u);
+}
+
+template <int T> __device__ __forceinline__ float f8_quotient(float v, const F8Block& b) {
+  const float x = ldexpf(v, b.shift);
+  const float h = F8_TOP * x;
+  float t = x * b.inv;
+  if constexpr (T != F32) return copysignf(fmaf(fmaf(-t, b.top, h), b.rcp, t), v);   // a zero keeps its sign
+  const float l = fmaf(F8_TOP, x, -h);
+  t = fmaf(fmaf(-t, b.top, h) + l, b.rcp, t);
+  const float rest = fmaf(-t, b.top, h) + l;
+  const uint32_t bits = f32_bits(t);
+  if ((bits & 0x7ffffu) == 0 && rest != 0.f && t != 0.f) t = bits_f32((rest > 0.f) == (t > 0.f) ? bits + 1 : bits - 1);
+  return copysignf(t, v);
+}
+
+// 4 codes, the first in the lowest byte
+__device__ __forceinline__ uint32_t f8_codes(float a, float b, float c, float d) {
+  int w = 0;
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, w, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+
+// Largest of the 16 lanes of a row (quads, then the quads of a half, then the halves).
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = quad_max(v);
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xf, 0xf, true));          // row_half_mirror
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xf, 0xf, true));       // row_mirror
+}
+
+template <int T> __device__ __forceinline__ void load8_or_zero(const typename Elem<T>::type* p, bool have, float v[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  if (have) load8<T>(p, v);
+}
+
+// Blocks of 128 along a row: a lane takes 8 elements, 16 lanes a block (the
+// last block of a row may have idle ones), so a wave's codes are 512 contiguous
+// bytes.  n: 16-lane groups, kb of them a row.
+template <int T>
+__global__ __launch_bounds__(EW_THREADS) void f8_quantize_rows_kernel(const typename Elem<T>::type* __restrict__ x,
+                                                                      int64_t ldx, int K, int kb, int64_t n,
+                                                                      uint8_t* __restrict__ codes,
+                                                                      float* __restrict__ scales) {
+  const int64_t step = (int64_t)gridDim.x * (EW_THREADS / 16);
+  const int lane = threadIdx.x & 15;
+  for (int64_t i = (int64_t)blockIdx.x * (EW_THREADS / 16) + (threadIdx.x >> 4); i < n; i += step) {
+    const int64_t r = i / kb;
+    const int k = (int)(i - r * kb) * 128 + lane * 8;
+    float v[8];
+    load8_or_zero<T>(x + r * ldx + k, k < K, v);
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, f32_bits(v[j]) & 0x7fffffffu);
+    top = row_max(top);
+    const F8Block b = f8_block(top);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f8_quotient<T>(v[j], b);
+    const u2 c = {f8_codes(v[0], v[1], v[2], v[3]), f8_codes(v[4], v[5], v[6], v[7])};
+    if (k < K) *reinterpret_cast<u2*>(codes + r * K + k) = b.finite ? c : u2{0, 0};
+    if (lane == 0) scales[i] = f8_scale(top);
+  }
+}
+
+// Tiles of 128 x 128: those whose block spans rows, and those that are turned
+// over.  A lane takes 8 columns of 4 consecutive rows, so that 4 codes of a
+// column are a word.  Largest magnitudes go from lane to lane over a wave's 16
+// rows and through LDS over the waves; turned codes go through LDS in rows of
+// 33 words (a wave's writes touch the 64 banks once), and are stored 32 bytes a
+// lane.  M rows of x; `wide` is the pitch of the turned codes, M rounded up to
+// 16, zeros past M.
+template <int T, bool BLOCK, bool TURN>
+__global__ __launch_bounds__(512) void f8_quantize_tiles_kernel(const typename Elem<T>::type* __restrict__ x,
+                                                                int64_t ldx, int M, int K, int wide,
+                                                                uint8_t* __restrict__ codes,
+                                                                float* __restrict__ scales) {
+  constexpr int PITCH = 33;
+  __shared__ uint32_t turned[TURN ? 128 * PITCH : 1];
+  __shared__ uint32_t tops[8 * 128];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int c8 = tid & 15, r4 = tid >> 4;                     // columns 8 c8.., rows 4 r4..
+  const int mb = blockIdx.y, kblk = blockIdx.x;
+  const int k = kblk * 128 + c8 * 8, m = mb * 128 + r4 * 4;
+  float v[4][8];
+  uint32_t top[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load8_or_zero<T>(x + (int64_t)(m + i) * ldx + k, k < K && m + i < M, v[i]);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    top[j] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top[j] = max(top[j], f32_bits(v[i][j]) & 0x7fffffffu);
+  }
+  uint32_t one = 0;
+  if constexpr (BLOCK) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) one = max(one, top[j]);
+    one = row_max(one);
+    one = max(one, (uint32_t)__shfl_xor((int)one, 16));
+    one = max(one, (uint32_t)__shfl_xor((int)one, 32));
+    if (lane == 0) tops[wave] = one;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) one = max(one, tops[w]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      top[j] = max(top[j], (uint32_t)__shfl_xor((int)top[j], 16));
+      top[j] = max(top[j], (uint32_t)__shfl_xor((int)top[j], 32));
+      if (lane < 16) tops[wave * 128 + c8 * 8 + j] = top[j];
+    }
+    __syncthreads();
+    if (tid < 128) {
+      uint32_t t = tops[tid];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) t = max(t, tops[w * 128 + tid]);
+      tops[tid] = t;     // this lane alone reads and writes the column's first word here
+    }
+    __syncthreads();
+  }
+  F8Block b;
+  if constexpr (BLOCK) b = f8_block(one);
+  uint32_t word[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (!BLOCK) b = f8_block(tops[c8 * 8 + j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i][j] = f8_quotient<T>(v[i][j], b);
+    if constexpr (TURN) {
+      word[j] = b.finite ? f8_codes(v[0][j], v[1][j], v[2][j], v[3][j]) : 0u;
+      turned[(c8 * 8 + j) * PITCH + r4] = word[j];
+    }
+  }
+  const int kbs = (K + 127) >> 7, mbs = (M + 127) >> 7;
+  if constexpr (BLOCK) {
+    if (tid == 0) scales[TURN ? (int64_t)kblk * mbs + mb : (int64_t)mb * kbs + kblk] = f8_scale(one);
+  } else {
+    if (tid < 128 && kblk * 128 + tid < K) scales[(int64_t)(kblk * 128 + tid) * mbs + mb] = f8_scale(tops[tid]);
+  }
+  if constexpr (!TURN) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u2 c = {f8_codes(v[i][0], v[i][1], v[i][2], v[i][3]), f8_codes(v[i][4], v[i][5], v[i][6], v[i][7])};
+      if (k < K && m + i < M) *reinterpret_cast<u2*>(codes + (int64_t)(m + i) * K + k) = b.finite ? c : u2{0, 0};
+    }
+  } else {
+    __syncthreads();
+    const int col = tid >> 2, part = tid & 3;
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = turned[col * PITCH + part * 8 + i];
+    uint8_t* to = codes + (int64_t)(kblk * 128 + col) * wide + mb * 128 + part * 32;
+    if (kblk * 128 + col < K) {
+      if (mb * 128 + part * 32 < wide) *reinterpret_cast<u4*>(to) = u4{w[0], w[1], w[2], w[3]};
+      if (mb * 128 + part * 32 + 16 < wide) *reinterpret_cast<u4*>(to + 16) = u4{w[4], w[5], w[6], w[7]};
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// products
+// ---------------------------------------------------------------------------
+// What is done with the products: stored (with the residual), gated, or turned
+// into the gradients of the two gated projections.
+constexpr int PRODUCT = 0, GATED = 1, GRAD = 2;
+
+struct F8Args {
+  const char* x; const float* xs; const uint8_t* w; const float* ws;
+  const char* resid; char* y;
+  const char* dh;                   // GRAD: [M, F]
+  int64_t ldx_bytes, ldr, ldy, ldd; // x row pitch in bytes, the others in elements
+  int M, N, K, F;                   // N: columns of y; F: features of the gated forms
+  int w_rows, kb;                   // rows of W, blocks of 128 along K
+  int y_type, act;
+};
+
+// The gate's value g s(t) and its slope s + g s (1 - s) t', with the logistic
+// function s and t = g (silu) or 2 sqrt(2 / pi) (g + 0.044715 g^3) (gelu in its
+// tanh form: (1 + tanh z) / 2 is s(2 z)).  e = exp(-|t|) <= 1 gives s and 1 - s
+// without overflow or cancellation.  Past |g| = 200 s (1 - s) is 0, and g is
+// held there so that it does not meet an infinite factor.
+struct Gate { float value, slope; };
+__device__ __forceinline__ Gate gate(float g, int act) {
+  constexpr float C = 1.5957691216057308f, D = 0.044715f;     // 2 sqrt(2 / pi)
+  const float t = act == QG_ACT_SILU ? g : C * (g + D * g * g * g);
+  const float e = __builtin_amdgcn_exp2f(-fabsf(t) * 1.4426950408889634f);
+  const float r = __builtin_amdgcn_rcpf(1.f + e);
+  const float s = t >= 0.f ? r : e * r, s1 = t >= 0.f ? e * r : r;
+  const float h = fminf(fmaxf(g, -200.f), 200.f);
+  const float dt = act == QG_ACT_SILU ? 1.f : C * (1.f + 3.f * D * h * h);
+  return {g * s, s + h * (s * s1) * dt};
+}
+
+// C consecutive features of row m from feature f on: their two projections to
+// what is stored.
+template <int MODE, int YT, int C>
+__device__ __forceinline__ void store_gated_as(const F8Args& a, int m, int f, float (&g)[C], float (&u)[C]) {
+  typedef typename Elem<YT>::type E;
+  if constexpr (MODE == GATED) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) g[i] = gate(g[i], a.act).value * u[i];
+    store_cols_as<YT, C>(a, m, f, g, 1.f);
+  } else {
+    E d[C];
+    get(reinterpret_cast<const E*>(a.dh) + (int64_t)m * a.ldd + f, d);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const Gate v = gate(g[i], a.act);
+      const float dh = to_f32(d[i]);
+      g[i] = dh * u[i] * v.slope;
+      u[i] = dh * v.value;
+    }
+    store_cols_as<YT, C>(a, m, f, g, 1.f);
+    store_cols_as<YT, C>(a, m, a.F + f, u, 1.f);
+  }
+}
+template <int MODE, int C>
+__device__ __forceinline__ void store_gated(const F8Args& a, int m, int f, float (&g)[C], float (&u)[C]) {
+  if (a.y_type == F32) store_gated_as<MODE, F32, C>(a, m, f, g, u);
+  else if (a.y_type == F16) store_gated_as<MODE, F16, C>(a, m, f, g, u);
+  else store_gated_as<MODE, BF16, C>(a, m, f, g, u);
+}
+
+// 8 codes -> 8 exact 16-bit values (E4M3 lies within fp16's and bf16's numbers)
+__device__ __forceinline__ b8 f8_to_bf16(uint32_t lo, uint32_t hi) {
+  const b2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
+  const b2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
+  const b2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
+  const b2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+  return b8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+__device__ __forceinline__ h8 f8_to_f16(uint32_t lo, uint32_t hi) {
+  const h2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false);
+  const h2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true);
+  const h2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false);
+  const h2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true);
+  return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// 16 x 16 outputs, 32 of k: 8 codes of W a lane against 8 elements of x, 16-bit
+// or (in x's first two words) codes.  Converted codes and their products are
+// exact in fp32.
+template <int XT> __device__ __forceinline__ f4 mfma_16(uint32_t lo, uint32_t hi, u4 x, f4 c) {
+  if constexpr (XT == BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_to_bf16(lo, hi), __builtin_bit_cast(b8, x), c, 0, 0, 0);
+  else if constexpr (XT == F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(f8_to_f16(lo, hi), __builtin_bit_cast(h8, x), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(f8_to_f16(lo, hi), f8_to_f16(x.x, x.y), c, 0, 0, 0);
+}
+
+// LDS of a wave for a chunk of 512 k of x: whole direct loads of a kilobyte
+// (two rows of codes, one 16-bit row)
+template <int XT> __host__ __device__ constexpr int f8_x_bytes(int M) {
+  const int rows = M < 16 ? M : 16;
+  return 1024 * (XT == F8 ? (rows + 1) / 2 : rows);
+}
+
+// Few rows: bound by the weights' bytes.  A workgroup owns a block of 16 columns
+// of y (rows of W; of a gated form 16 of the gate's and the same 16 of the
+// other projection) and up to 16 rows of it; its NW waves take K's chunks of
+// 512 in turn and are summed through LDS in wave order.  Lane l = 16 g + r of a
+// wave loads the eight 16-byte pieces 4 u + g of a chunk of row r of W straight
+// to registers and converts them there.  x goes straight to the wave's own LDS; row r keeps
+// its piece c at place c ^ r, so 16 rows' reads touch the 64 banks once.  Each
+// block of 128 has its own sum, which joins the others times its scales.  W is
+// the first operand, so a lane ends with four consecutive outputs of one row.
+// MULTI: a workgroup goes through several column blocks, or its waves through
+// several chunks, the next weights on their way meanwhile.
+template <int XT, int MODE, int NW, bool MULTI, bool ROWS>
+__global__ __launch_bounds__(NW * 64) void f8_rows_kernel(F8Args a) {
+  constexpr int NT = MODE == PRODUCT ? 1 : 2;
+  constexpr int XC = XT == F8 ? 512 : 1024;       // bytes of an x row a chunk
+  extern __shared__ __align__(1024) uint8_t rows_lds[];
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int np = a.K >> 4;                        // 16-byte pieces of a row of codes
+  const int chunks = (np + 31) >> 5, turns = (chunks + NW - 1) / NW;   // a wave's chunks: wave, wave + NW, ..
+  const int blocks = MODE == PRODUCT ? (a.N + 15) >> 4 : a.F >> 4;
+  const int m0 = blockIdx.y * 16, rows = min(a.M - m0, 16), rr = min(r, rows - 1);
+  const int xbytes = f8_x_bytes<XT>(a.M);
+  uint8_t* const xl = rows_lds + wave * xbytes;
+  auto w_row = [&](int nb, int j) { return (MODE == PRODUCT ? 0 : j * a.F) + nb * 16; };   // a block's first row of W
+
+  struct W { u4 c[NT][8]; };
+  auto load_w = [&](int nb, int c, W& w) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const uint8_t* wp = a.w + (int64_t)min(w_row(nb, j) + r, a.w_rows - 1) * a.K;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) w.c[j][u] = *reinterpret_cast<const u4*>(wp + (int64_t)min(c * 32 + 4 * u + g, np - 1) * 16);
+    }
+  };
+  auto dma = [](const char* from, uint8_t* to) { __builtin_amdgcn_global_load_lds((gptr)from, (lptr)to, 16, 0, 0); };
+  // x: a whole chunk of the rows there are (past K: a row's last piece again)
+  auto load_x = [&](int c) {
+    if constexpr (XT == F8) {
+      for (int i = 0; i < rows; i += 2) {
+        const int row = i + (lane >> 5);
+        dma(a.x + (int64_t)(m0 + min(row, rows - 1)) * a.ldx_bytes + (int64_t)min(c * 32 + ((lane & 31) ^ row), np - 1) * 16,
+            xl + i * XC);
+      }
+    } else {
+      for (int i = 0; i < rows; ++i)
+        dma(a.x + (int64_t)(m0 + i) * a.ldx_bytes + (int64_t)min(c * 64 + (lane ^ i), np * 2 - 1) * 16, xl + i * XC);
+    }
+  };
+  // the scales of a chunk's four blocks: this lane's row of x, and the rows of
+  // W behind its four outputs (one for all of them where a block has 128 rows)
+  constexpr int SR = ROWS ? 4 : 1;
+  struct S { float x[4], w[NT][SR][4]; };
+  auto load_scales = [&](int nb, int c, S& s) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int kb = min(c * 4 + b, a.kb - 1);
+      s.x[b] = XT == F8 ? a.xs[(int64_t)(m0 + rr) * a.kb + kb] : 1.f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < SR; ++i) {
+          const int64_t row = ROWS ? min(w_row(nb, j) + 4 * g + i, a.w_rows - 1) : w_row(nb, j) >> 7;
+          s.w[j][i][b] = a.ws[row * a.kb + kb];
+        }
+    }
+  };
+
+  W w0, w1;
+  S s;
+  f4 acc[NT];
+  int nb = blockIdx.x, turn = 0, buf = 0;
+  if (chunks > 0) {
+    if (turns == 1 && wave < chunks) load_x(wave);
+    load_w(nb, min(wave, chunks - 1), w0);
+  }
+  // one chunk of one block: its products, and after a block's last chunk the sums
+  auto item = [&](auto MORE, W& w, W& next) {   // MORE: another item follows
+    const int c = wave + turn * NW;
+    const bool last = turn + 1 >= turns;
+    if (c < chunks) {
+      load_scales(nb, c, s);
+      if (turns > 1) load_x(c);
+    }
+    // The next item's weights (a wave without a chunk loads some).  All other loads are waited for: those stay on their way.
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (decltype(MORE)::value) {
+      load_w(last ? nb + (int)gridDim.x : nb, min(last ? wave : c + NW, chunks - 1), next);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      wait_loads<NT * 8>();
+    } else {
+      wait_loads<0>();
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (turn == 0) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (c < chunks) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (c * 32 + 8 * b >= np) break;
+        u4 xv[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int p = 8 * b + 4 * h + g;
+          const bool past = c * 32 + p >= np;   // zero operands
+          if constexpr (XT == F8) {
+            u4 v = *reinterpret_cast<const u4*>(xl + rr * XC + ((p ^ rr) * 16));
+            if (past) v = u4{0, 0, 0, 0};
+            xv[2 * h] = u4{v.x, v.y, 0, 0};
+            xv[2 * h + 1] = u4{v.z, v.w, 0, 0};
+          } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              xv[2 * h + q] = *reinterpret_cast<const u4*>(xl + rr * XC + (((2 * p + q) ^ rr) * 16));
+              if (past) xv[2 * h + q] = u4{0, 0, 0, 0};
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            if (past) w.c[j][2 * b + h] = u4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          f4 part = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            part = mfma_16<XT>(w.c[j][2 * b + q / 2][2 * (q & 1)], w.c[j][2 * b + q / 2][2 * (q & 1) + 1], xv[q], part);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(part[i], s.x[b] * s.w[j][ROWS ? i : 0][b], acc[j][i]);
+        }
+      }
+    }
+    if (!last) {
+      wait_lds();   // x has been read, its place may be sent for again
+      asm volatile("" ::: "memory");
+      ++turn;
+      return;
+    }
+    // the waves' sums; two buffers, so one barrier a block does
+    f4* part = reinterpret_cast<f4*>(rows_lds + NW * xbytes) + buf * (NW * NT * 64);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[(wave * NT + j) * 64 + lane] = acc[j];
+    lds_barrier();
+    if (wave == buf % NW) {
+      f4 v[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        v[j] = part[j * 64 + lane];
+#pragma unroll
+        for (int k = 1; k < NW; ++k) v[j] += part[(k * NT + j) * 64 + lane];
+      }
+      const int n = nb * 16 + 4 * g;
+      if (r < rows && n < (MODE == PRODUCT ? a.N : a.F)) {
+        float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+        if constexpr (MODE == PRODUCT) {
+          store_cols<4>(a, m0 + r, n, o, 1.f);
+        } else {
+          float u[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+          store_gated<MODE, 4>(a, m0 + r, n, o, u);
+        }
+      }
+    }
+    buf ^= 1;
+    turn = 0;
+    nb += gridDim.x;
+  };
+  int left = nb < blocks ? ((blocks - 1 - nb) / (int)gridDim.x + 1) * max(turns, 1) : 0;
+  if constexpr (MULTI) {
+    for (; left > 2; left -= 2) {
+      item(std::true_type{}, w0, w1);
+      item(std::true_type{}, w1, w0);
+    }
+    if (left == 2) {
+      item(std::true_type{}, w0, w1);
+      item(std::false_type{}, w1, w0);
+      left = 0;
+    }
+  }
+  if (left == 1) item(std::false_type{}, w0, w1);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+struct F8Plan { int tile, nw; int64_t workgroups; bool fits; };
+
+F8Plan plan_f8(int mode, int M, int N, int K, int x_type) {
+  F8Plan p = {0, 1, 0, true};
+  if (M == 0 || N == 0) return p;
+  const int64_t chunks = ((int64_t)K + 511) / 512;
+  // a wave for every chunk, as far as LDS holds x and the sums for them
+  p.nw = chunks <= 1 ? 1 : chunks <= 2 ? 2 : chunks <= 4 ? 4 : chunks <= 8 ? 8 : 16;
+  const int rows = std::min(M, 16), nt = mode == PRODUCT ? 1 : 2;
+  while (p.nw * ((x_type == F8 ? (rows + 1) / 2 : rows) + 2 * nt) > 160) p.nw /= 2;
+  p.workgroups = ((int64_t)M + 15) / 16 * (((int64_t)N + 15) / 16);
+  p.fits = ((int64_t)M + 15) / 16 <= 65535;
+  return p;
+}
+
+template <int XT, int MODE, int NW, bool ROWS> void launch_rows(const F8Args& a, hipStream_t s) {
+  constexpr int NT = MODE == PRODUCT ? 1 : 2;
+  const int64_t gy = ((int64_t)a.M + 15) / 16;
+  const size_t lds = (size_t)NW * f8_x_bytes<XT>(a.M) + 2 * NW * NT * 1024;
+  // column blocks a workgroup takes: no more workgroups than keep 32 waves on every CU
+  const int64_t blocks = MODE == PRODUCT ? ((int64_t)a.N + 15) / 16 : a.F / 16;
+  const int64_t slots = 256 * 32 / NW, share = a.K == 0 ? 1 : (blocks * gy + slots - 1) / slots;
+  const dim3 grid((unsigned)((blocks + share - 1) / share), (unsigned)gy);
+  if (share == 1 && a.K <= 512 * NW)
+    hipLaunchKernelGGL((f8_rows_kernel<XT, MODE, NW, false, ROWS>), grid, dim3(NW * 64), lds, s, a);
+  else
+    hipLaunchKernelGGL((f8_rows_kernel<XT, MODE, NW, true, ROWS>), grid, dim3(NW * 64), lds, s, a);
+}
+
+template <int XT, int MODE, bool ROWS> void launch_f8(const F8Args& a, const F8Plan& p, hipStream_t s) {
+  if (p.nw == 1) return launch_rows<XT, MODE, 1, ROWS>(a, s);
+  if (p.nw == 2) return launch_rows<XT, MODE, 2, ROWS>(a, s);
+  if (p.nw == 4) return launch_rows<XT, MODE, 4, ROWS>(a, s);
+  if (p.nw == 8) return launch_rows<XT, MODE, 8, ROWS>(a, s);
+  return launch_rows<XT, MODE, 16, ROWS>(a, s);
+}
+
+template <int MODE> int run_f8(const F8Args& a, int x_type, int w_block, void* stream) {
+  const F8Plan p = plan_f8(MODE, a.M, MODE == PRODUCT ? a.N : a.F, a.K, x_type);
+  if (!p.fits) return QG_E_UNSUPPORTED;
+  int st = device_present();
+  if (st != QG_OK) return st;
+  const void* ptrs[7] = {a.x, a.xs, a.w, a.ws, a.resid, a.dh, a.y};
+  st = check_device_pointers(ptrs, 7);
+  if (st != QG_OK) return st;
+  clear_pending_error();
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if constexpr (MODE == PRODUCT) {
+    if (w_block == 1) {
+      launch_f8<F8, MODE, true>(a, p, s);
+      return launch_status();
+    }
+  }
+  if (x_type == F8) launch_f8<F8, MODE, false>(a, p, s);
+  else if (x_type == BF16) launch_f8<BF16, MODE, false>(a, p, s);
+  else launch_f8<F16, MODE, false>(a, p, s);
+  return launch_status();
+}
+
+// Checks shared by the three products; fills the fields that all use.  N: the
+// columns of y, w_rows: the rows of W.
+int setup_f8(const void* x, int ldx, int x_type, const float* xs, const uint8_t* w, const float* ws, int w_block, int M,
+             int N, int w_rows, int K, void* y, int ldy, int y_type, F8Args* a) {
+  if (x_type != F16 && x_type != BF16 && x_type != F8) return QG_E_ARG;
+  if (!float_type(y_type) || M < 0 || N < 0 || K < 0 || K % 16) return QG_E_ARG;
+  if ((w_block != 1 && w_block != 128) || (w_block == 1 && x_type != F8)) return QG_E_ARG;
+  if (M == 0 || N == 0) return QG_OK;
+  if (M > INT_MAX - 512 || w_rows > INT_MAX - 512 || K > INT_MAX - 512) return QG_E_UNSUPPORTED;   // the kernels round them up in 32 bits
+  if (!y || ldy < N) return QG_E_ARG;
+  if (K > 0) {
+    if (!x || !w || !ws || (x_type == F8) != (xs != nullptr)) return QG_E_ARG;
+    if (x_type == F8 ? ldx != K : ldx < K) return QG_E_ARG;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(ws, 4) || !aligned(xs, 4) || ldx % 8) return QG_E_ALIGN;
+  }
+  if (!aligned(y, 16)) return QG_E_ALIGN;
+  *a = F8Args{};
+  a->x = reinterpret_cast<const char*>(x);
+  a->xs = xs; a->w = w; a->ws = ws;
+  a->ldx_bytes = (int64_t)ldx * (x_type == F8 ? 1 : 2);
+  a->M = M; a->N = N; a->K = K; a->w_rows = w_rows; a->kb = (K + 127) / 128;
+  a->y = reinterpret_cast<char*>(y);
+  a->ldy = ldy; a->y_type = y_type;
+  return QG_OK;
+}
+
+int check_act(int act, int F) { return (act == QG_ACT_SILU || act == QG_ACT_GELU_TANH) && F >= 0 && F % 16 == 0 && F <= INT_MAX / 2 ? QG_OK : QG_E_ARG; }
+
+template <int T>
+void launch_quantize(const void* v, int ldx, int M, int K, int block, bool turn, uint8_t* codes, float* scales, hipStream_t s) {
+  typedef typename Elem<T>::type E;
+  const E* x = reinterpret_cast<const E*>(v);
+  const int kb = (K + 127) / 128;
+  if (block == 1 && !turn) {
+    const int64_t n = (int64_t)M * kb;
+    const dim3 grid((unsigned)std::min<int64_t>((n + EW_THREADS / 16 - 1) / (EW_THREADS / 16), 256 * 16));
+    hipLaunchKernelGGL(f8_quantize_rows_kernel<T>, grid, dim3(EW_THREADS), 0, s, x, (int64_t)ldx, K, kb, n, codes, scales);
+    return;
+  }
+  const dim3 grid((unsigned)kb, (unsigned)(((int64_t)M + 127) / 128)), threads(512);
+  const int wide = (M + 15) / 16 * 16;
+  if (!turn) hipLaunchKernelGGL((f8_quantize_tiles_kernel<T, true, false>), grid, threads, 0, s, x, (int64_t)ldx, M, K, wide, codes, scales);
+  else if (block == 1) hipLaunchKernelGGL((f8_quantize_tiles_kernel<T, false, true>), grid, threads, 0, s, x, (int64_t)ldx, M, K, wide, codes, scales);
+  else hipLaunchKernelGGL((f8_quantize_tiles_kernel<T, true, true>), grid, threads, 0, s, x, (int64_t)ldx, M, K, wide, codes, scales);
+}
+
+}  // namespace
+}  // namespace qg
+
+using namespace qg;
+
+extern "C" int qf8_quantize(const void* x, int ldx, int x_type, int M, int K, int block, int transpose, uint8_t* codes,
+                            float* scales, void* stream) {
+  if (!float_type(x_type) || M < 0 || K < 0 || K % 16 || (block != 1 && block != 128) || (transpose != 0 && transpose != 1))
+    return QG_E_ARG;
+  if (M == 0 || K == 0) return QG_OK;
+  if (!x || !codes || !scales || ldx < K) return QG_E_ARG;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4) || ldx % 8) return QG_E_ALIGN;
+  if (M > INT_MAX - 512 || K > INT_MAX - 512) return QG_E_UNSUPPORTED;
+  if ((block != 1 || transpose) && (M > 65535 * 128 || K > (1 << 30) - 128)) return QG_E_UNSUPPORTED;   // the tiles' grid
+  int st = device_present();
+  if (st != QG_OK) return st;
+  const void* ptrs[3] = {x, codes, scales};
+  st = check_device_pointers(ptrs, 3);
+  if (st != QG_OK) return st;
+  clear_pending_error();
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (x_type == F16) launch_quantize<F16>(x, ldx, M, K, block, transpose, codes, scales, s);
+  else if (x_type == BF16) launch_quantize<BF16>(x, ldx, M, K, block, transpose, codes, scales, s);
+  else launch_quantize<F32>(x, ldx, M, K, block, transpose, codes, scales, s);
+  return launch_status();
+}
+
+extern "C" int qf8_gemm(const void* x, int ldx, int x_type, const float* x_scales, const uint8_t* w, const float* w_scales,
+                        int w_block, const void* residual, int ldr, int M, int N, int K, void* y, int ldy, int y_type,
+                        void* stream) {
+  F8Args a;
+  int st = setup_f8(x, ldx, x_type, x_scales, w, w_scales, w_block, M, N, N, K, y, ldy, y_type, &a);
+  if (st != QG_OK) return st;
+  if (M == 0 || N == 0) return QG_OK;
+  if (residual) {
+    if (ldr < N || (residual == y && ldr != ldy)) return QG_E_ARG;
+    if (!aligned(residual, 16)) return QG_E_ALIGN;
+    a.resid = reinterpret_cast<const char*>(residual);
+    a.ldr = ldr;
+  }
+  return run_f8<PRODUCT>(a, x_type, w_block, stream);
+}
+
+extern "C" int qf8_gated(const void* x, int ldx, int x_type, const float* x_scales, const uint8_t* w, const float* w_scales,
+                         int act, int M, int F, int K, void* h, int ldh, int h_type, void* stream) {
+  F8Args a;
+  int st = check_act(act, F);
+  if (st == QG_OK) st = setup_f8(x, ldx, x_type, x_scales, w, w_scales, 128, M, F, 2 * F, K, h, ldh, h_type, &a);
+  if (st != QG_OK) return st;
+  if (M == 0 || F == 0) return QG_OK;
+  a.F = F;
+  a.act = act;
+  return run_f8<GATED>(a, x_type, 128, stream);
+}
+
+extern "C" int qf8_gated_grad(const void* dh, int lddh, const void* x, int ldx, int x_type, const float* x_scales,
+                              const uint8_t* w, const float* w_scales, int act, int M, int F, int K, void* d, int ldd,
+                              int d_type, void* stream) {
+  F8Args a;
+  int st = check_act(act, F);
+  if (st == QG_OK) st = setup_f8(x, ldx, x_type, x_scales, w, w_scales, 128, M, 2 * F, 2 * F, K, d, ldd, d_type, &a);
+  if (st != QG_OK) return st;
+  if (M == 0 || F == 0) return QG_OK;
+  if (!dh || lddh < F) return QG_E_ARG;
+  if (!aligned(dh, 16)) return QG_E_ALIGN;
+  a.F = F;
+  a.act = act;
+  a.dh = reinterpret_cast<const char*>(dh);
+  a.ldd = lddh;
+  return run_f8<GRAD>(a, x_type, 128, stream);
+}

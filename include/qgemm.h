@@ -408,6 +408,99 @@ int qmx_gemm_grouped(const void* x, int ldx, int x_type, const uint8_t* x_scales
 int qmx_plan(int M, int N, int K, int E, int x_type, int out[4]);
 
 /*
+ * 8-bit floating point with an fp32 scale for blocks of 128, and the gated
+ * feed-forward block on it.
+ *
+ * A matrix [R, K] in this form is two arrays, both row-major and contiguous:
+ *   codes  uint8 [R, K]   E4M3 (OCP 8-bit floating point: 4 exponent and 3
+ *                         mantissa bits, largest 448, no infinities, NaN 0x7f
+ *                         and 0xff).
+ *   scales fp32 [R, ceil(K/128)]           block 1: a factor for 128 elements of a row, or
+ *          fp32 [ceil(R/128), ceil(K/128)] block 128: one for 128 x 128.
+ * Blocks at the edges are what is left.  A value is its code times its block's
+ * scale.  The usual form of activations and gradients is block 1, of weights
+ * block 128.  The products read it as it is: there is no packing step.
+ *
+ * Conventions: those of the MXFP4 operators above (no workspace, any stream,
+ * capturable), with these differences.  K % 16 == 0.  Scales are 4-byte
+ * aligned.  The types are numbered on from qg_mx_type_t.
+ */
+enum { QG_F8_E4M3 = 4 };
+
+/* What gates a feed-forward block: silu g / (1 + exp(-g)), or gelu in its tanh
+ * form g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))). */
+typedef enum { QG_ACT_SILU = 0, QG_ACT_GELU_TANH = 1 } qg_act_t;
+
+/*
+ * qf8_quantize: x [M, K] -> codes and scales.
+ * Per block, with A its largest magnitude (at least 2^-100): the scale is A /
+ * 448 rounded to fp32, a code the nearest to 448 v / A, ties to the even one,
+ * its sign kept.  A block that holds an infinity or a NaN gets a NaN scale and
+ * codes 0, so it reads back as NaN.
+ *   x         [device, in] x_type QG_MX_F16, QG_MX_BF16 or QG_MX_F32, leading dimension ldx >= K, ldx % 8 == 0.
+ *   block     1 or 128.
+ *   transpose 0, or 1: codes and scales are those of the transposed matrix [K, Mp], Mp = M rounded up to a
+ *             multiple of 16, with zero codes past M; blocks of 128 run along M.  (What the products that sum
+ *             over M read: a weight's gradient over the tokens.)
+ *   codes, scales [device, out].
+ * M == 0 or K == 0 is a no-op.
+ * Errors: QG_E_ARG, QG_E_ALIGN, QG_E_UNSUPPORTED (M or K beyond 2^31 - 513; block 128 or transposed: M beyond
+ * 65535 * 128 or K beyond 2^30 - 128), QG_E_DEVICE, QG_E_NOT_DEVICE.
+ */
+int qf8_quantize(const void* x, int ldx, int x_type, int M, int K, int block, int transpose, uint8_t* codes,
+                 float* scales, void* stream);
+
+/*
+ * qf8_gemm: y[M, N] = x[M, K] . W[N, K]^T (+ residual), W in E4M3.  The codes'
+ * products are summed in fp32 over a block of 128 k, the blocks' sums times
+ * their scales in fp32; one rounding to y_type at the end.
+ *   x        [device, in] x_type QG_MX_F16 or QG_MX_BF16 with leading dimension ldx >= K, ldx % 8 == 0, or
+ *            QG_F8_E4M3: codes (then ldx == K) with x_scales [M, ceil(K/128)] (block 1).
+ *   x_scales NULL unless x_type is QG_F8_E4M3.
+ *   w, w_scales [device, in] [N, K] in blocks of w_block: 128, or (with 8-bit x) 1.
+ *   residual [device, in] y_type [M, N] with leading dimension ldr >= N, or NULL.  It may be y
+ *            itself when ldr == ldy.
+ *   y        [device, out] y_type QG_MX_F16, QG_MX_BF16 or QG_MX_F32, leading dimension ldy >= N.
+ * M == 0 or N == 0 is a no-op; K == 0 writes zeros (plus the residual).
+ * Sums are added in a fixed order: equal inputs give equal bits.
+ * Errors: QG_E_ARG, QG_E_ALIGN, QG_E_UNSUPPORTED (sizes beyond 2^31 - 513; more pieces of y than a grid
+ * holds), QG_E_DEVICE, QG_E_NOT_DEVICE.
+ */
+int qf8_gemm(const void* x, int ldx, int x_type, const float* x_scales, const uint8_t* w, const float* w_scales,
+             int w_block, const void* residual, int ldr, int M, int N, int K, void* y, int ldy, int y_type,
+             void* stream);
+
+/*
+ * qf8_gated: h[M, F] = act(x . Wg^T) * (x . Wu^T), both projections, the
+ * activation and the product in one kernel.  Neither projection is rounded or
+ * written to memory.
+ *   x, x_scales as qf8_gemm.
+ *   w, w_scales [device, in] [2F, K] in blocks of 128: Wg is its first F rows, Wu the others.  F % 16 == 0 (a
+ *            block may hold rows of both).
+ *   act      qg_act_t.
+ *   h        [device, out] h_type QG_MX_F16, QG_MX_BF16 or QG_MX_F32, leading dimension ldh >= F.
+ * M == 0 or F == 0 is a no-op; K == 0 writes zeros.  Errors as qf8_gemm.
+ */
+int qf8_gated(const void* x, int ldx, int x_type, const float* x_scales, const uint8_t* w, const float* w_scales,
+              int act, int M, int F, int K, void* h, int ldh, int h_type, void* stream);
+
+/*
+ * qf8_gated_grad: the backward pass of qf8_gated up to its projections.  With
+ * g = x . Wg^T and u = x . Wu^T (computed again, in the same kernel):
+ *   d[:, 0:F] = dh * u * act'(g),   d[:, F:2F] = dh * act(g).
+ * The gradients follow from d [M, 2F] as products: dx = d . W (qf8_gemm with
+ * the transposed weight), dW = d^T . x (qf8_gemm of both operands quantised with
+ * transpose = 1).
+ *   dh       [device, in] d_type [M, F], leading dimension lddh >= F.
+ *   x, x_scales, w, w_scales, act as qf8_gated.
+ *   d        [device, out] d_type [M, 2F], leading dimension ldd >= 2F; not dh's memory.
+ * M == 0 or F == 0 is a no-op.  Errors as qf8_gemm.
+ */
+int qf8_gated_grad(const void* dh, int lddh, const void* x, int ldx, int x_type, const float* x_scales,
+                   const uint8_t* w, const float* w_scales, int act, int M, int F, int K, void* d, int ldd,
+                   int d_type, void* stream);
+
+/*
  * Measurement helpers: the ceilings a qGEMM kernel is read against, taken on
  * the device it runs on (the hot-op microbenchmarks of the TinyLoop README,
  * "Validation", and the phase timings of its "Quick CLI Tour", "Benchmark").
