@@ -490,19 +490,278 @@ __global__ __launch_bounds__(NW * 64) void f8_rows_kernel(F8Args a) {
 }
 
 // ---------------------------------------------------------------------------
+// more rows
+// ---------------------------------------------------------------------------
+// 16 x 16 outputs, 128 of k: both operands 32 codes a lane.  Any order of k is
+// right as long as both follow it.  The matrix cores add the products of 8
+// codes of a lane on a grid of 2^(e - 13), e the largest sum of two exponents
+// among them, and cut what is finer (measured; whatever the instruction's
+// shape).  The rest of the sum is as exact as fp32.
+__device__ __forceinline__ f4 mfma_f8(u4 a0, u4 a1, u4 b0, u4 b1) {
+  const i8v a = {(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
+  const i8v b = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// Where a direct load takes what lies past K from.
+__device__ const u4 f8_zeros = {0, 0, 0, 0};
+
+// Which tile a workgroup has: numbered row tile fastest within blocks of 8 row
+// tiles, a range of numbers to an XCD (workgroup b runs on XCD b % 8), so that
+// tiles whose operands an XCD's L2 holds run together.
+__device__ __forceinline__ bool f8_tile(int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int64_t total = (int64_t)tiles_m * tiles_n;
+  const int xcd = blockIdx.x & 7;
+  const int64_t id = total * xcd / 8 + (blockIdx.x >> 3);
+  if (id >= total * (xcd + 1) / 8) return false;
+  const int64_t per = (int64_t)8 * tiles_n;
+  const int blk = (int)(id / per), in = (int)(id - blk * per);
+  const int bm = min(8, tiles_m - blk * 8);
+  tm = blk * 8 + in % bm;
+  tn = in / bm;
+  return true;
+}
+
+// Stores a wave's MI x NI blocks of 16 x 16 (lane 16 g + r: columns 4 g .. 4 g +
+// 3 of row r) at row m0 and column (gated forms: feature) n0.  Each strip of 16 rows
+// passes through LDS (the wave's own `strip`, rows padded by 16 bytes), so that
+// a lane stores 8 consecutive outputs.  Gated forms have gate and other
+// projection in turn, 16 features each.
+template <int MODE, int YT, int MI, int NI>
+__device__ __forceinline__ void f8_store_as(const F8Args& a, uint8_t* strip, int m0, int n0, const f4 (&acc)[MI][NI]) {
+  constexpr int PITCH = 16 * NI + 4, PARTS = MODE == PRODUCT ? 1 : 2;
+  constexpr int LANES = 2 * NI / PARTS, ROWS = 64 / LANES;   // lanes a row, rows at a time
+  const int lane = threadIdx.x & 63, c = lane % LANES;
+  float* s = reinterpret_cast<float*>(strip);
+  const float* from = s + (MODE == PRODUCT ? c * 8 : (c >> 1) * 32 + (c & 1) * 8);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) *reinterpret_cast<f4*>(s + (lane & 15) * PITCH + 16 * j + 4 * (lane >> 4)) = acc[i][j];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const int n = n0 + c * 8;
+#pragma unroll
+    for (int p = 0; p < (16 + ROWS - 1) / ROWS; ++p) {
+      const int r = p * ROWS + lane / LANES, m = m0 + i * 16 + r;
+      if (r < 16 && m < a.M && n < (MODE == PRODUCT ? a.N : a.F)) {
+        float v[8];
+        __builtin_memcpy(v, from + r * PITCH, sizeof(v));
+        if constexpr (MODE == PRODUCT) {
+          store_cols_as<YT, 8>(a, m, n, v, 1.f);
+        } else {
+          float u[8];
+          __builtin_memcpy(u, from + r * PITCH + 16, sizeof(u));
+          store_gated_as<MODE, YT, 8>(a, m, n, v, u);
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+// x and W stream through a ring of RING LDS stages of 128 k: a workgroup of WM
+// x WN waves, each MI x NI blocks of 16 x 16 outputs.  The loads go straight to
+// LDS, RING - 1 stages ahead; a stage is one block of the scales, which come
+// with it.  A row's 16-byte pieces change places by the row's number, so that
+// the fragment reads of 16 consecutive rows touch the 64 banks evenly: rows of
+// codes are 128 bytes (piece c at c ^ (row / 2 % 8)), 16-bit rows 256 (c ^ (row %
+// 16)).  Pieces past K are zeros.  The one barrier a stage says both that
+// everyone's loads of it have arrived and that the stage before has been read.
+// FAST: 8-bit matrix instructions; else the codes are converted to 16 bits.
+// W is the first operand: a lane's outputs run along a row of y.
+template <int XT, bool FAST, int MODE, bool ROWS, int MI, int NI, int WM, int WN, int RING>
+__global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args a, int tiles_m, int tiles_n) {
+  constexpr int NW = WM * WN, TM = 16 * MI * WM, TN = 16 * NI * WN, TF = MODE == PRODUCT ? TN : TN / 2;
+  constexpr bool C8 = XT == F8;
+  constexpr int XB = C8 ? 128 : 256, XR = 1024 / XB;         // bytes of an x row a stage, rows a direct load brings
+  constexpr int QA = TM / XR / NW, QB = TN / 8 / NW, QD = QA + QB;   // direct loads of 1 KiB a wave and stage
+  static_assert(QA * XR * NW == TM && QB * 8 * NW == TN, "rows split evenly over the waves");
+  constexpr int SROWS = (C8 ? TM : 0) + TN, SOFF = C8 ? TM : 0;      // rows with scales; W's first
+  static_assert(SROWS % 64 == 0, "a load brings the scales of 64 rows");
+  constexpr int QS = (SROWS / 64 + NW - 1) / NW;              // such loads a wave and stage
+  constexpr int PIECES = TM * XB + TN * 128, STAGE = PIECES + SROWS * 4;
+  static_assert(NW * 16 * (16 * NI + 4) * 4 <= RING * STAGE, "the strips of f8_store_as");
+  // one array: with two, the compiler waits for every direct load before each read
+  __shared__ __align__(1024) uint8_t smem[RING * STAGE];
+  int tm, tn;
+  if (!f8_tile(tiles_m, tiles_n, tm, tn)) return;
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int m0 = tm * TM, n0 = tn * TF;                       // n0: first column, or feature
+  const int stages = a.kb;
+
+  // row p of the tile's W (gated forms: 16 features of the gate, the same of the other, ..)
+  auto w_row = [&](int p) {
+    if constexpr (MODE == PRODUCT) return min(n0 + p, a.w_rows - 1);
+    else return (p >> 4 & 1) * a.F + min(n0 + (p >> 5) * 16 + (p & 15), a.F - 1);
+  };
+  // direct loads: lane l brings a 16-byte piece of row l / 8 of 8 (16-bit x: row l / 16 of 4)
+  const char* src[QD];
+  int at[QD];             // the piece's place in the row's stage, in bytes
+#pragma unroll
+  for (int q = 0; q < QD; ++q) {
+    if (q < QA) {
+      const int row = (wave * QA + q) * XR + lane / (64 / XR);
+      at[q] = C8 ? ((lane & 7) ^ (row >> 1 & 7)) * 16 : ((lane & 15) ^ (row & 15)) * 16;
+      src[q] = a.x + (int64_t)min(m0 + row, a.M - 1) * a.ldx_bytes + at[q];
+    } else {
+      const int row = (wave * QB + q - QA) * 8 + (lane >> 3);
+      at[q] = ((lane & 7) ^ (row >> 1 & 7)) * 16;
+      src[q] = reinterpret_cast<const char*>(a.w) + (int64_t)w_row(row) * a.K + at[q];
+    }
+  }
+  // scales: row l of 64 (waves to spare bring the same rows again)
+  const float* ssrc[QS];
+#pragma unroll
+  for (int q = 0; q < QS; ++q) {
+    const int p = (wave * QS + q) % (SROWS / 64) * 64 + lane;
+    ssrc[q] = C8 && p < TM ? a.xs + (int64_t)min(m0 + p, a.M - 1) * a.kb
+                           : a.ws + (int64_t)(ROWS ? w_row(p - SOFF) : w_row(p - SOFF) >> 7) * a.kb;
+  }
+  auto place = [&](uint8_t* to, int q) { return to + (q < QA ? (wave * QA + q) * 1024 : TM * XB + (wave * QB + q - QA) * 1024); };
+  // stage `it` into place `to`; past the last one the last again, into a place that is not read any more
+  auto issue = [&](int it, uint8_t* to) {
+    it = min(it, stages - 1);
+    const bool whole = (it + 1) * 128 <= a.K;
+#pragma unroll
+    for (int q = 0; q < QD; ++q) {
+      const int per = q < QA ? XB : 128;
+      const char* p = src[q] + (int64_t)it * per;
+      if (!whole && it * per + at[q] >= a.K * (per / 128)) p = reinterpret_cast<const char*>(&f8_zeros);
+      __builtin_amdgcn_global_load_lds((gptr)p, (lptr)place(to, q), 16, 0, 0);
+    }
+#pragma unroll
+    for (int q = 0; q < QS; ++q)
+      __builtin_amdgcn_global_load_lds((gptr)(ssrc[q] + it), (lptr)(to + PIECES + (wave * QS + q) % (SROWS / 64) * 256), 4, 0, 0);
+  };
+  auto barrier = [] {
+    asm volatile("" ::: "memory");   // no LDS access moves across it
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // fragments: lane 16 g + r reads pieces 2 g and 2 g + 1 of row r of codes, pieces 4 g .. 4 g + 3 of 16-bit rows
+  int foff[2], xoff[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) foff[h] = r * 128 + (((2 * g + h) ^ (r >> 1 & 7)) * 16);
+#pragma unroll
+  for (int h = 0; h < 4; ++h) xoff[h] = r * 256 + (((4 * g + h) ^ r) * 16);
+  f4 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+  for (int it = 0; it < RING - 1; ++it) issue(it, smem + it * STAGE);
+  int cur = 0, fill = RING - 1;
+#pragma unroll 1
+  for (int it = 0; it < stages; ++it) {
+    wait_loads<(RING - 2) * (QD + QS)>();
+    barrier();
+    issue(it + RING - 1, smem + fill * STAGE);
+    fill = fill + 1 == RING ? 0 : fill + 1;
+    const uint8_t* const st = smem + cur * STAGE;
+    const float* const sc = reinterpret_cast<const float*>(st + PIECES);
+    cur = cur + 1 == RING ? 0 : cur + 1;
+    u4 b[NI][2];
+    f4 sw[NI];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int row = (wn * NI + j) * 16;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) b[j][h] = *reinterpret_cast<const u4*>(st + TM * XB + row * 128 + foff[h]);
+      if constexpr (ROWS) sw[j] = *reinterpret_cast<const f4*>(sc + SOFF + row + 4 * g);
+      else sw[j].x = sc[SOFF + row];
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int row = (wm * MI + i) * 16;
+      u4 x[C8 ? 2 : 4];
+#pragma unroll
+      for (int h = 0; h < (C8 ? 2 : 4); ++h)
+        x[h] = *reinterpret_cast<const u4*>(st + row * XB + (C8 ? foff[h & 1] : xoff[h]));
+      const float sx = C8 ? sc[row + r] : 1.f;
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        f4 part = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (FAST) {
+          part = mfma_f8(b[j][0], b[j][1], x[0], x[1]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            part = mfma_16<XT>(b[j][q >> 1][2 * (q & 1)], b[j][q >> 1][2 * (q & 1) + 1],
+                               C8 ? u4{x[q >> 1][2 * (q & 1)], x[q >> 1][2 * (q & 1) + 1], 0, 0} : x[q], part);
+        }
+        if constexpr (ROWS) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(part[k], sx * sw[j][k], acc[i][j][k]);
+        } else {
+          const float f = C8 ? sx * sw[j].x : sw[j].x;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(part[k], f, acc[i][j][k]);
+        }
+      }
+    }
+  }
+  wait_loads<0>();   // nothing is on its way to LDS any more
+  barrier();
+  uint8_t* const strip = smem + wave * (16 * (16 * NI + 4) * 4);
+  const int m = m0 + wm * MI * 16, n = n0 + wn * NI * (MODE == PRODUCT ? 16 : 8);
+  if constexpr (FAST) {
+    f8_store_as<MODE, BF16, MI, NI>(a, strip, m, n, acc);
+  } else {
+    if (a.y_type == F32) f8_store_as<MODE, F32, MI, NI>(a, strip, m, n, acc);
+    else if (a.y_type == F16) f8_store_as<MODE, F16, MI, NI>(a, strip, m, n, acc);
+    else f8_store_as<MODE, BF16, MI, NI>(a, strip, m, n, acc);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 struct F8Plan { int tile, nw; int64_t workgroups; bool fits; };
 
-F8Plan plan_f8(int mode, int M, int N, int K, int x_type) {
+// What the tiles multiply with: 16-bit x, 8-bit x on converted codes, 8-bit x as it is.
+enum { KIND_16 = 0, KIND_EXACT = 1, KIND_FAST = 2 };
+struct F8Tile { int rows, cols, threads; };
+constexpr F8Tile F8_TILES[3][3] = {{{64, 64, 256}, {128, 128, 512}, {128, 256, 512}},
+                                   {{64, 64, 256}, {128, 128, 512}, {256, 256, 512}},
+                                   {{64, 64, 256}, {128, 128, 256}, {256, 256, 512}}};
+
+int64_t f8_grid(int M, int64_t w_rows, const F8Tile& t) {
+  return (((int64_t)M + t.rows - 1) / t.rows * ((w_rows + t.cols - 1) / t.cols) + 7) / 8 * 8;
+}
+
+// N: columns of y, or features of a gated form.
+F8Plan plan_f8(int mode, int M, int N, int K, int kind) {
   F8Plan p = {0, 1, 0, true};
   if (M == 0 || N == 0) return p;
-  const int64_t chunks = ((int64_t)K + 511) / 512;
+  const int64_t chunks = ((int64_t)K + 511) / 512, w_rows = mode == PRODUCT ? N : 2 * (int64_t)N;
+  if (K > 0) {
+    if (M > 16) p.tile = 1;
+    if (M > 64 && (int64_t)M * w_rows >= 128 * 128 * 256) p.tile = 2;
+    if (M > 128 && (int64_t)M * w_rows >= 256 * 256 * 200) p.tile = 3;
+    const int forced = env_int("QF8_TILE", -1);
+    if (forced >= 0 && forced <= 3) p.tile = forced;
+  }
+  if (p.tile) {
+    const F8Tile& t = F8_TILES[kind][p.tile - 1];
+    p.workgroups = ((int64_t)M + t.rows - 1) / t.rows * ((w_rows + t.cols - 1) / t.cols);
+    p.fits = f8_grid(M, w_rows, t) * t.threads <= (int64_t)UINT32_MAX;
+    return p;
+  }
   // a wave for every chunk, as far as LDS holds x and the sums for them
   p.nw = chunks <= 1 ? 1 : chunks <= 2 ? 2 : chunks <= 4 ? 4 : chunks <= 8 ? 8 : 16;
   const int rows = std::min(M, 16), nt = mode == PRODUCT ? 1 : 2;
-  while (p.nw * ((x_type == F8 ? (rows + 1) / 2 : rows) + 2 * nt) > 160) p.nw /= 2;
+  while (p.nw * ((kind != KIND_16 ? (rows + 1) / 2 : rows) + 2 * nt) > 160) p.nw /= 2;
   p.workgroups = ((int64_t)M + 15) / 16 * (((int64_t)N + 15) / 16);
+  // 16 waves have 128 registers each: enough for one chunk a wave and one block a workgroup, not for the next ones' weights
+  if (p.nw == 16 && (chunks > 16 || p.workgroups > 256 * 2)) p.nw = 8;
   p.fits = ((int64_t)M + 15) / 16 <= 65535;
   return p;
 }
@@ -515,22 +774,46 @@ template <int XT, int MODE, int NW, bool ROWS> void launch_rows(const F8Args& a,
   const int64_t blocks = MODE == PRODUCT ? ((int64_t)a.N + 15) / 16 : a.F / 16;
   const int64_t slots = 256 * 32 / NW, share = a.K == 0 ? 1 : (blocks * gy + slots - 1) / slots;
   const dim3 grid((unsigned)((blocks + share - 1) / share), (unsigned)gy);
-  if (share == 1 && a.K <= 512 * NW)
-    hipLaunchKernelGGL((f8_rows_kernel<XT, MODE, NW, false, ROWS>), grid, dim3(NW * 64), lds, s, a);
-  else
-    hipLaunchKernelGGL((f8_rows_kernel<XT, MODE, NW, true, ROWS>), grid, dim3(NW * 64), lds, s, a);
+  if constexpr (NW <= 8) {
+    if (share > 1 || a.K > 512 * NW) {
+      hipLaunchKernelGGL((f8_rows_kernel<XT, MODE, NW, true, ROWS>), grid, dim3(NW * 64), lds, s, a);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((f8_rows_kernel<XT, MODE, NW, false, ROWS>), grid, dim3(NW * 64), lds, s, a);
 }
 
-template <int XT, int MODE, bool ROWS> void launch_f8(const F8Args& a, const F8Plan& p, hipStream_t s) {
-  if (p.nw == 1) return launch_rows<XT, MODE, 1, ROWS>(a, s);
-  if (p.nw == 2) return launch_rows<XT, MODE, 2, ROWS>(a, s);
-  if (p.nw == 4) return launch_rows<XT, MODE, 4, ROWS>(a, s);
-  if (p.nw == 8) return launch_rows<XT, MODE, 8, ROWS>(a, s);
-  return launch_rows<XT, MODE, 16, ROWS>(a, s);
+template <int XT, bool FAST, int MODE, bool ROWS, int MI, int NI, int WM, int WN, int RING>
+void launch_tiles(const F8Args& a, hipStream_t s) {
+  constexpr F8Tile t = {16 * MI * WM, 16 * NI * WN, WM * WN * 64};
+  static_assert(t.rows == F8_TILES[FAST ? KIND_FAST : XT == F8 ? KIND_EXACT : KIND_16][0].rows ||
+                t.rows >= F8_TILES[FAST ? KIND_FAST : XT == F8 ? KIND_EXACT : KIND_16][1].rows, "as planned");
+  const dim3 grid((unsigned)f8_grid(a.M, a.w_rows, t));
+  hipLaunchKernelGGL((f8_tile_kernel<XT, FAST, MODE, ROWS, MI, NI, WM, WN, RING>), grid, dim3(t.threads), 0, s, a,
+                     (a.M + t.rows - 1) / t.rows, (int)(((int64_t)a.w_rows + t.cols - 1) / t.cols));
+}
+
+template <int XT, bool FAST, int MODE, bool ROWS> void launch_f8(const F8Args& a, const F8Plan& p, hipStream_t s) {
+  if (p.tile == 1) return launch_tiles<XT, FAST, MODE, ROWS, 2, 2, 2, 2, XT == F8 ? 4 : 3>(a, s);
+  if constexpr (FAST) {
+    if (p.tile == 2) return launch_tiles<XT, FAST, MODE, ROWS, 4, 4, 2, 2, 4>(a, s);
+    if (p.tile == 3) return launch_tiles<XT, FAST, MODE, ROWS, 8, 4, 2, 4, 2>(a, s);
+  } else {
+    if (p.tile == 2) return launch_tiles<XT, FAST, MODE, ROWS, 4, 2, 2, 4, XT == F8 ? 4 : 3>(a, s);
+    if (p.tile == 3) return launch_tiles<XT, FAST, MODE, ROWS, XT == F8 ? 8 : 4, 4, 2, 4, 2>(a, s);
+  }
+  if constexpr (!FAST) {
+    if (p.nw == 1) return launch_rows<XT, MODE, 1, ROWS>(a, s);
+    if (p.nw == 2) return launch_rows<XT, MODE, 2, ROWS>(a, s);
+    if (p.nw == 4) return launch_rows<XT, MODE, 4, ROWS>(a, s);
+    if (p.nw == 8) return launch_rows<XT, MODE, 8, ROWS>(a, s);
+    return launch_rows<XT, MODE, 16, ROWS>(a, s);
+  }
 }
 
 template <int MODE> int run_f8(const F8Args& a, int x_type, int w_block, void* stream) {
-  const F8Plan p = plan_f8(MODE, a.M, MODE == PRODUCT ? a.N : a.F, a.K, x_type);
+  const int kind = x_type != F8 ? KIND_16 : a.y_type == BF16 && w_block == 128 ? KIND_FAST : KIND_EXACT;
+  const F8Plan p = plan_f8(MODE, a.M, MODE == PRODUCT ? a.N : a.F, a.K, kind);
   if (!p.fits) return QG_E_UNSUPPORTED;
   int st = device_present();
   if (st != QG_OK) return st;
@@ -541,13 +824,14 @@ template <int MODE> int run_f8(const F8Args& a, int x_type, int w_block, void* s
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if constexpr (MODE == PRODUCT) {
     if (w_block == 1) {
-      launch_f8<F8, MODE, true>(a, p, s);
+      launch_f8<F8, false, MODE, true>(a, p, s);
       return launch_status();
     }
   }
-  if (x_type == F8) launch_f8<F8, MODE, false>(a, p, s);
-  else if (x_type == BF16) launch_f8<BF16, MODE, false>(a, p, s);
-  else launch_f8<F16, MODE, false>(a, p, s);
+  if (x_type == BF16) launch_f8<BF16, false, MODE, false>(a, p, s);
+  else if (x_type == F16) launch_f8<F16, false, MODE, false>(a, p, s);
+  else if (kind == KIND_FAST && p.tile) launch_f8<F8, true, MODE, false>(a, p, s);
+  else launch_f8<F8, false, MODE, false>(a, p, s);
   return launch_status();
 }
 

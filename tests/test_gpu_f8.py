@@ -10,6 +10,13 @@ nearest), the factor of a block (two scales) and its product 2^-24 each, a
 residual's addition 2^-24.  A stored value is off by half a step more (eps / 2 of
 its type, or half its smallest subnormal).
 
+With 8-bit x, W in blocks of 128 and bf16 results the larger kernels use 8-bit
+matrix instructions, which add the products of 8 consecutive k on a grid of
+2^(e - 13), e the largest sum of two codes' exponents among them (a subnormal
+code's is -6), and cut what is finer.  The product that has e is a multiple of
+2^(e - 6), so at most seven are cut: CUT() bounds that by 7 2^-13 times the
+largest |x| times the largest |w| of every 8.
+
 The gate g s(t), s the logistic function: e = exp(-|t|) is off by (|t| + 1) 2^-23
 of itself (the product with log2 e rounds twice, exp2 is good to a unit), 1 + e,
 its reciprocal and their product by 2.5 2^-23 more, and t, for gelu a polynomial
@@ -58,6 +65,21 @@ def stored(ref, dtype):
 
 def sums(K, mag):
     return (K + -(-K // 128) + 4) * U * mag
+
+
+def eights(codes, scales):
+    """The largest magnitude of every 8 consecutive k, at least 2^-6 times the scale."""
+    R, K = codes.shape
+    top = np.maximum(np.abs(f8ref.VALUES[codes]), 2.0 ** -6).reshape(R, K // 8, 8).max(axis=2)
+    s = np.repeat(np.abs(scales.astype(np.float64)), 16, axis=1)[:, :K // 8]
+    return top * (s if scales.shape[0] == R else np.repeat(s, 128, axis=0)[:R])
+
+
+def cut(x, xs, wc, ws, yt):
+    """What 8-bit matrix instructions may leave out (see above); 0 where they are not used."""
+    if xs is None or yt != BF16 or (ws.shape[0] == wc.shape[0] and len(wc) > 1):
+        return 0.0
+    return 7 * 2.0 ** -13 * (eights(codes_of(x), xs.cpu().numpy()) @ eights(wc, ws).T)
 
 
 def inside(y, ref, tol):
@@ -245,7 +267,7 @@ def test_gemm_random_with_residual_and_strides(kind, yt, M, N, K):
     out = torch.full((M, N + 5), 9.0, dtype=yt, device=DEV)
     ref, mag = f8ref.f8_gemm_ref(xv, f8ref.f8_values(wc, ws), residual=f64(r[:, :N]))
     qgm.f8_gemm(x, dev(wc), dev(ws), x_scales=xs, out=out[:, :N], residual=r.to(DEV)[:, :N])
-    inside(out[:, :N], ref, sums(K, mag))
+    inside(out[:, :N], ref, sums(K, mag) + cut(x, xs, wc, ws, yt))
     assert bool((out[:, N:] == 9).all())
     # in place: the residual is the output itself
     y = r.to(DEV).contiguous()[:, :N].clone()
@@ -323,6 +345,105 @@ def test_gemm_empty(kind, M, N, K):
     assert not bool(qgm.f8_gemm(x, w, ws, x_scales=xs, out_dtype=F32).any())
 
 
+# every kernel whatever the rule would take: sizes around their tiles, K that ends inside a stage of 128 and on it
+EVERY = [(1, 129, 512), (70, 257, 528), (17, 64, 992), (130, 300, 1024), (260, 70, 1600), (3, 40, 128), (66, 130, 336),
+         (5, 17, 16), (129, 513, 480), (33, 100, 2512), (300, 530, 144), (600, 1100, 272)]
+
+
+@pytest.mark.parametrize("tile", range(4))
+@pytest.mark.parametrize("kind", KINDS + ["rows"])
+@pytest.mark.parametrize("M,N,K", EVERY)
+def test_gemm_every_kernel(monkeypatch, tile, kind, M, N, K):
+    monkeypatch.setenv("QF8_TILE", str(tile))
+    rng = np.random.default_rng(M + N + K)
+    block, xk = (1, "f8") if kind == "rows" else (128, kind)
+    wc, ws = exact_f8(rng, N, K, block)
+    ws *= 2.0 ** rng.integers(-1, 2, ws.shape)
+    x, xs, xv = make_x(rng, xk, M, K, exact=True)
+    ref = f8ref.f8_gemm_ref(xv, f8ref.f8_values(wc, ws))[0]
+    for yt in (F32, F16, BF16):
+        out = torch.full((M + 1, N + 3), 9.0, dtype=yt, device=DEV)
+        qgm.f8_gemm(x, dev(wc), dev(ws), x_scales=xs, out=out[:M, :N])
+        assert np.array_equal(f64(out[:M, :N]), rounded(ref, yt))
+        assert bool((out[M] == 9).all()) and bool((out[:, N:] == 9).all())
+    # codes and scales of every size, a NaN code and a NaN scale that reach their own columns only
+    wc, ws = random_f8(rng, N, K, block)
+    wc[N // 2, K - 1] = 255
+    x, xs, xv = make_x(rng, xk, M, K)
+    with np.errstate(invalid="ignore"):
+        ref, mag = f8ref.f8_gemm_ref(xv, f8ref.f8_values(wc, ws))
+    keep = np.arange(N) != N // 2
+    left = cut(x, xs, np.where(wc == 255, 0, wc).astype(np.uint8), ws, BF16)
+    for yt in (F32, BF16):
+        y = qgm.f8_gemm(x, dev(wc), dev(ws), x_scales=xs, out_dtype=yt)
+        assert bool(torch.isnan(y[:, N // 2]).all())
+        tol = sums(K, mag) + (left if yt == BF16 else 0.0)
+        inside(y[:, torch.from_numpy(keep).to(DEV)], ref[:, keep], tol[:, keep])
+
+
+@pytest.mark.parametrize("tile", range(4))
+@pytest.mark.parametrize("kind", KINDS)
+def test_gemm_past_k_is_not_read_into_sums(monkeypatch, tile, kind):
+    # rows whose neighbours in memory are NaN: x with a wide pitch, the last row of W before other codes
+    monkeypatch.setenv("QF8_TILE", str(tile))
+    rng = np.random.default_rng(tile)
+    M, N, K = 37, 50, 176
+    x, xs, xv = make_x(rng, kind, M, K)
+    if xs is None:
+        wide = torch.full((M + 1, K + 96), float("nan"), dtype=x.dtype, device=DEV)
+        wide[:M, :K] = x
+        x = wide[:M, :K]
+    else:
+        wide = torch.full((M + 300, K), 127, dtype=torch.uint8, device=DEV)
+        wide[:M] = x.view(torch.uint8)
+        x = wide.view(CODE)[:M]
+    wc, ws = random_f8(rng, N, K, 128)
+    w = torch.full((N + 300, K), 127, dtype=torch.uint8, device=DEV)
+    w[:N] = dev(wc).view(torch.uint8)
+    ref, mag = f8ref.f8_gemm_ref(xv, f8ref.f8_values(wc, ws))
+    for yt in (F32, BF16):
+        inside(qgm.f8_gemm(x, w.view(CODE)[:N], dev(ws), x_scales=xs, out_dtype=yt), ref,
+               sums(K, mag) + cut(x, xs, wc, ws, yt))
+
+
+@pytest.mark.parametrize("tile", range(4))
+@pytest.mark.parametrize("kind", ["bf16", "f8"])
+def test_gemm_far_rows(monkeypatch, tile, kind):
+    # rows of x, of W and of y that lie more than 4 GiB into their arrays
+    monkeypatch.setenv("QF8_TILE", str(tile))
+    rng = np.random.default_rng(tile)
+    K, far = 8192, 600000
+    xc, s, xv = make_x(rng, kind, 3, K)
+    x = torch.zeros(far, K, dtype=torch.uint8 if kind == "f8" else BF16, device=DEV)
+    x[far - 3:] = xc.view(torch.uint8) if kind == "f8" else xc
+    xs = None
+    if kind == "f8":
+        x, xs = x.view(CODE), torch.ones(far, K // 128, device=DEV)
+        xs[far - 3:] = s
+    wc, ws = random_f8(rng, 48, K, 128)
+    y = qgm.f8_gemm(x, dev(wc), dev(ws), x_scales=xs, out_dtype=F32)
+    ref, mag = f8ref.f8_gemm_ref(xv, f8ref.f8_values(wc, ws))
+    inside(y[far - 3:], ref, sums(K, mag))
+    assert not bool(y[:far - 3].any())
+    del x, xs, y
+    w = torch.zeros(far, K, dtype=torch.uint8, device=DEV)
+    w[far - 48:] = dev(wc).view(torch.uint8)
+    wsc = torch.ones(-(-far // 128), K // 128, device=DEV)
+    wsc[-1:] = dev(ws)
+    out = torch.full((3, far), 9.0, device=DEV)
+    assert far % 128 == 64
+    qgm.f8_gemm(xc, w.view(CODE), wsc, x_scales=s, out=out)
+    inside(out[:, far - 48:], ref, sums(K, mag))
+    assert not bool(out[:, :far - 48].any())
+    del w, out
+    big = torch.zeros(40, 1 << 27, dtype=F32, device=DEV)      # 20 GiB: y's own rows
+    row = xc[:1].expand(40, K).contiguous()
+    rs = None if s is None else s[:1].expand(40, K // 128).contiguous()
+    qgm.f8_gemm(row, dev(wc), dev(ws), x_scales=rs, out=big[:, :48])
+    inside(big[39:, :48], ref[:1], sums(K, mag[:1]))
+    assert not bool(big[:, 48:64].any())
+
+
 # ------------------------------------------------------- the gated block
 
 ACTS = ["silu", "gelu_tanh"]
@@ -330,12 +451,13 @@ GATED = [(1, 16, 16), (1, 208, 2048), (3, 48, 96), (16, 64, 272), (17, 144, 512)
          (65, 272, 240), (130, 176, 528), (257, 400, 384), (520, 1040, 272)]
 
 
-def gate_tolerances(x, w, act, K):
-    """(h, its tolerance before storing, and what the gradient's needs)."""
+def gate_tolerances(x, w, act, K, left=0.0):
+    """(h, its tolerance before storing, and what the gradient's needs); left: what cut() gives."""
     F = w.shape[0] // 2
     h, g, u = f8ref.gated_ref(x, w, act)
     mag = np.abs(x) @ np.abs(w).T
-    eg, eu = sums(K, mag[:, :F]), sums(K, mag[:, F:])
+    e = sums(K, mag) + left
+    eg, eu = e[:, :F], e[:, F:]
     a, da = f8ref.act_ref(g, act)
     t = np.abs(g) if act == "silu" else 1.5957691216057308 * np.abs(g + 0.044715 * g ** 3)
     ea = (4 * t + 6) * U * np.abs(a) + 2.0 ** -126 * np.abs(g) + 1.2 * eg
@@ -343,31 +465,38 @@ def gate_tolerances(x, w, act, K):
     return h, th, (g, u, a, da, eg, eu, ea, t)
 
 
+@pytest.mark.parametrize("tile", [None, 0, 1, 2, 3])
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("M,F,K", GATED)
-def test_gated(kind, act, M, F, K):
+def test_gated(monkeypatch, tile, kind, act, M, F, K):
+    if tile is not None:
+        monkeypatch.setenv("QF8_TILE", str(tile))
     rng = np.random.default_rng(M + F + K)
     x, xs, xv = make_x(rng, kind, M, K)
     wc, ws = random_f8(rng, 2 * F, K, 128, size=0.02 if kind != "f8" else 0.005)
-    h, tol, _ = gate_tolerances(xv, f8ref.f8_values(wc, ws), act, K)
+    wv = f8ref.f8_values(wc, ws)
     for yt in (F32, XTYPE.get(kind, BF16)):
+        h, tol, _ = gate_tolerances(xv, wv, act, K, cut(x, xs, wc, ws, yt))
         out = torch.full((M + 1, F + 3), 9.0, dtype=yt, device=DEV)
         y = qgm.f8_gated(x, dev(wc), dev(ws), x_scales=xs, act=act, out=out[:M, :F])
         inside(y, h, tol)
         assert bool((out[M] == 9).all()) and bool((out[:, F:] == 9).all())
 
 
+@pytest.mark.parametrize("tile", [None, 0, 1, 2, 3])
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("M,F,K", GATED)
-def test_gated_grad(kind, act, M, F, K):
+def test_gated_grad(monkeypatch, tile, kind, act, M, F, K):
+    if tile is not None:
+        monkeypatch.setenv("QF8_TILE", str(tile))
     rng = np.random.default_rng(M + F + K)
     x, xs, xv = make_x(rng, kind, M, K)
     wc, ws = random_f8(rng, 2 * F, K, 128, size=0.02 if kind != "f8" else 0.005)
     wv = f8ref.f8_values(wc, ws)
-    _, _, (g, u, a, da, eg, eu, ea, t) = gate_tolerances(xv, wv, act, K)
     for yt in (F32, XTYPE.get(kind, BF16)):
+        _, _, (g, u, a, da, eg, eu, ea, t) = gate_tolerances(xv, wv, act, K, cut(x, xs, wc, ws, yt))
         dh = torch.randn(M, F + 2, device=DEV).to(yt)[:, :F]
         ref = f8ref.gated_grad_ref(f64(dh), xv, wv, act)
         # the slope's two terms: s, and g s (1 - s) t', which is what da leaves over
@@ -430,8 +559,9 @@ def test_training_step():
     xq, xs = qgm.f8_quantize(x)
     h = block(xq, x_scales=xs, out_dtype=BF16)
     xv = f8ref.f8_values(codes_of(xq), xs.cpu().numpy())
-    wv = f8ref.f8_values(codes_of(block.codes), block.scales.cpu().numpy())
-    ref, tol, _ = gate_tolerances(xv, wv, "gelu_tanh", K)
+    wc, ws = codes_of(block.codes), block.scales.cpu().numpy()
+    wv = f8ref.f8_values(wc, ws)
+    ref, tol, _ = gate_tolerances(xv, wv, "gelu_tanh", K, cut(xq, xs, wc, ws, BF16))
     inside(h, ref, tol)
     d = block.grad(dh, xq, x_scales=xs)
     dx = back(d)                                            # 16-bit gradients ..
@@ -440,7 +570,8 @@ def test_training_step():
     dq, ds = qgm.f8_quantize(d)                             # .. or in 8 bits
     dv = f8ref.f8_values(codes_of(dq), ds.cpu().numpy())
     ref, mag = f8ref.f8_gemm_ref(dv, wv.T)
-    inside(back(dq, x_scales=ds, out_dtype=BF16), ref, sums(2 * F, mag))
+    left = cut(dq, ds, codes_of(back.codes), back.scales.cpu().numpy(), BF16)
+    inside(back(dq, x_scales=ds, out_dtype=BF16), ref, sums(2 * F, mag) + left)
     dt, dts = qgm.f8_quantize(d, transpose=True)
     xt, xts = qgm.f8_quantize(x, transpose=True)
     total = torch.randn(2 * F, K, device=DEV)
