@@ -284,16 +284,18 @@ __device__ __forceinline__ h8 f8_to_f16(uint32_t lo, uint32_t hi) {
   return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-// 16 x 16 outputs, 32 of k: 8 codes of W a lane against 8 elements of x, 16-bit
-// or (in x's first two words) codes.  Converted codes and their products are
-// exact in fp32.
-template <int XT> __device__ __forceinline__ f4 mfma_16(uint32_t lo, uint32_t hi, u4 x, f4 c) {
+// 8 codes as 16-bit operands for x of type XT (codes: fp16).
+template <int XT> __device__ __forceinline__ u4 f8_to_16(uint32_t lo, uint32_t hi) {
+  if constexpr (XT == BF16) return __builtin_bit_cast(u4, f8_to_bf16(lo, hi));
+  else return __builtin_bit_cast(u4, f8_to_f16(lo, hi));
+}
+// 16 x 16 outputs, 32 of k, 8 16-bit elements a lane.  Converted codes and
+// their products are exact in fp32.
+template <int XT> __device__ __forceinline__ f4 mfma_16(u4 w, u4 x, f4 c) {
   if constexpr (XT == BF16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_to_bf16(lo, hi), __builtin_bit_cast(b8, x), c, 0, 0, 0);
-  else if constexpr (XT == F16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(f8_to_f16(lo, hi), __builtin_bit_cast(h8, x), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, w), __builtin_bit_cast(b8, x), c, 0, 0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(f8_to_f16(lo, hi), f8_to_f16(x.x, x.y), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, w), __builtin_bit_cast(h8, x), c, 0, 0, 0);
 }
 
 // LDS of a wave for a chunk of 512 k of x: whole direct loads of a kilobyte
@@ -416,8 +418,8 @@ __global__ __launch_bounds__(NW * 64) void f8_rows_kernel(F8Args a) {
           if constexpr (XT == F8) {
             u4 v = *reinterpret_cast<const u4*>(xl + rr * XC + ((p ^ rr) * 16));
             if (past) v = u4{0, 0, 0, 0};
-            xv[2 * h] = u4{v.x, v.y, 0, 0};
-            xv[2 * h + 1] = u4{v.z, v.w, 0, 0};
+            xv[2 * h] = f8_to_16<XT>(v.x, v.y);
+            xv[2 * h + 1] = f8_to_16<XT>(v.z, v.w);
           } else {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -434,7 +436,7 @@ __global__ __launch_bounds__(NW * 64) void f8_rows_kernel(F8Args a) {
           f4 part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            part = mfma_16<XT>(w.c[j][2 * b + q / 2][2 * (q & 1)], w.c[j][2 * b + q / 2][2 * (q & 1) + 1], xv[q], part);
+            part = mfma_16<XT>(f8_to_16<XT>(w.c[j][2 * b + q / 2][2 * (q & 1)], w.c[j][2 * b + q / 2][2 * (q & 1) + 1]), xv[q], part);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(part[i], s.x[b] * s.w[j][ROWS ? i : 0][b], acc[j][i]);
         }
@@ -503,9 +505,6 @@ __device__ __forceinline__ f4 mfma_f8(u4 a0, u4 a1, u4 b0, u4 b1) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
-// Where a direct load takes what lies past K from.
-__device__ const u4 f8_zeros = {0, 0, 0, 0};
-
 // Which tile a workgroup has: numbered row tile fastest within blocks of 8 row
 // tiles, a range of numbers to an XCD (workgroup b runs on XCD b % 8), so that
 // tiles whose operands an XCD's L2 holds run together.
@@ -563,14 +562,23 @@ __device__ __forceinline__ void f8_store_as(const F8Args& a, uint8_t* strip, int
   }
 }
 
+// A buffer of `bytes` (below 2^31) from `base` on: loads past its end give zeros.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer f8_buffer(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
+}
+constexpr uint32_t PAST = 0x80000000u;   // an offset past every buffer's end
+
 // x and W stream through a ring of RING LDS stages of 128 k: a workgroup of WM
 // x WN waves, each MI x NI blocks of 16 x 16 outputs.  The loads go straight to
-// LDS, RING - 1 stages ahead; a stage is one block of the scales, which come
-// with it.  A row's 16-byte pieces change places by the row's number, so that
-// the fragment reads of 16 consecutive rows touch the 64 banks evenly: rows of
-// codes are 128 bytes (piece c at c ^ (row / 2 % 8)), 16-bit rows 256 (c ^ (row %
-// 16)).  Pieces past K are zeros.  The one barrier a stage says both that
-// everyone's loads of it have arrived and that the stage before has been read.
+// LDS, RING stages ahead; a stage is one block of the scales, which come with
+// it.  A row's 16-byte pieces change places by the row's number, so that the
+// fragment reads touch the 64 banks evenly: rows of codes are 128 bytes (piece c
+// at c ^ (row / 2 % 8)), 16-bit rows 256 (c ^ (row % 16)).  Pieces past K and
+// rows past the last are zeros.  The one barrier a stage, before its last row of
+// blocks, says both that everyone's loads of the next stage have arrived and
+// that this one has been read: the next fragments of W and the first of x are
+// read, and the loads of stage it + RING sent for, while that row is multiplied.
 // FAST: 8-bit matrix instructions; else the codes are converted to 16 bits.
 // W is the first operand: a lane's outputs run along a row of y.
 template <int XT, bool FAST, int MODE, bool ROWS, int MI, int NI, int WM, int WN, int RING>
@@ -580,9 +588,11 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args a, int til
   constexpr int XB = C8 ? 128 : 256, XR = 1024 / XB;         // bytes of an x row a stage, rows a direct load brings
   constexpr int QA = TM / XR / NW, QB = TN / 8 / NW, QD = QA + QB;   // direct loads of 1 KiB a wave and stage
   static_assert(QA * XR * NW == TM && QB * 8 * NW == TN, "rows split evenly over the waves");
-  constexpr int SROWS = (C8 ? TM : 0) + TN, SOFF = C8 ? TM : 0;      // rows with scales; W's first
-  static_assert(SROWS % 64 == 0, "a load brings the scales of 64 rows");
-  constexpr int QS = (SROWS / 64 + NW - 1) / NW;              // such loads a wave and stage
+  // rows whose scales come with a stage: x's, and W's where each of its rows has its own (else they are the same for a
+  // wave's 16 columns, and come by scalar loads a stage ahead)
+  constexpr int SROWS = (C8 ? TM : 0) + (ROWS ? TN : 0), SOFF = C8 ? TM : 0;
+  static_assert(SROWS % 64 == 0 && SOFF % 64 == 0, "a load brings the scales of 64 rows, of x or of W");
+  constexpr int SL = SROWS / 64 > 0 ? SROWS / 64 : 1, QS = (SROWS / 64 + NW - 1) / NW, QALL = QD + QS;   // such loads, and a wave's
   constexpr int PIECES = TM * XB + TN * 128, STAGE = PIECES + SROWS * 4;
   static_assert(NW * 16 * (16 * NI + 4) * 4 <= RING * STAGE, "the strips of f8_store_as");
   // one array: with two, the compiler waits for every direct load before each read
@@ -594,120 +604,207 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args a, int til
   const int wm = wave / WN, wn = wave % WN;
   const int m0 = tm * TM, n0 = tn * TF;                       // n0: first column, or feature
   const int stages = a.kb;
+  const uint32_t xpitch = (uint32_t)a.ldx_bytes, wpitch = (uint32_t)a.K;
 
-  // row p of the tile's W (gated forms: 16 features of the gate, the same of the other, ..)
-  auto w_row = [&](int p) {
-    if constexpr (MODE == PRODUCT) return min(n0 + p, a.w_rows - 1);
-    else return (p >> 4 & 1) * a.F + min(n0 + (p >> 5) * 16 + (p & 15), a.F - 1);
-  };
-  // direct loads: lane l brings a 16-byte piece of row l / 8 of 8 (16-bit x: row l / 16 of 4)
-  const char* src[QD];
-  int at[QD];             // the piece's place in the row's stage, in bytes
+  // The tile's rows as buffers (the host sees to it that a tile's rows stay below 2^31 bytes).  Row p of the
+  // tile's W: of the gated forms 16 features of the gate, the same of the other projection, and so on; the two
+  // have a buffer each.
+  const int wrows = MODE == PRODUCT ? min(a.w_rows - n0, TN) : min(a.F - n0, TF);
+  const Buffer xb = f8_buffer(a.x + (int64_t)m0 * a.ldx_bytes, (int64_t)min(a.M - m0, TM) * a.ldx_bytes);
+  const uint8_t* const wbase = a.w + (int64_t)n0 * a.K;
+  // Direct load q of a wave brings eight rows of codes (or four 16-bit rows), lane l a piece of the (l / 8)th.  The
+  // piece's number depends on q by its parity only (16-bit rows: by q % 4), so offsets within a load are few and
+  // the rest is the same for all lanes.
+  constexpr int XV = C8 ? 2 : 4;
+  int xpiece[XV], wpiece[2];
 #pragma unroll
-  for (int q = 0; q < QD; ++q) {
-    if (q < QA) {
-      const int row = (wave * QA + q) * XR + lane / (64 / XR);
-      at[q] = C8 ? ((lane & 7) ^ (row >> 1 & 7)) * 16 : ((lane & 15) ^ (row & 15)) * 16;
-      src[q] = a.x + (int64_t)min(m0 + row, a.M - 1) * a.ldx_bytes + at[q];
-    } else {
-      const int row = (wave * QB + q - QA) * 8 + (lane >> 3);
-      at[q] = ((lane & 7) ^ (row >> 1 & 7)) * 16;
-      src[q] = reinterpret_cast<const char*>(a.w) + (int64_t)w_row(row) * a.K + at[q];
-    }
-  }
-  // scales: row l of 64 (waves to spare bring the same rows again)
-  const float* ssrc[QS];
+  for (int v = 0; v < XV; ++v)
+    xpiece[v] = C8 ? (lane & 7) ^ ((v * 4 + (lane >> 4)) & 7) : (lane & 15) ^ ((v * 4 + (lane >> 4)) & 15);
+#pragma unroll
+  for (int v = 0; v < 2; ++v) wpiece[v] = (lane & 7) ^ ((v * 4 + (lane >> 4)) & 7);
+  const uint32_t xlane = (lane / (64 / XR)) * xpitch, wlane = (lane >> 3) * wpitch;
+  // scales: rows 64 n .. of the tile's x, then of its W (waves to spare bring the same rows again)
+  const Buffer xsb = f8_buffer(C8 ? a.xs + (int64_t)m0 * a.kb : nullptr, C8 ? (int64_t)min(a.M - m0, TM) * a.kb * 4 : 0);
+  const Buffer wsb = f8_buffer(ROWS ? a.ws + (int64_t)n0 * a.kb : nullptr, ROWS ? (int64_t)wrows * a.kb * 4 : 0);
+  uint32_t soff[QS > 0 ? QS : 1];
 #pragma unroll
   for (int q = 0; q < QS; ++q) {
-    const int p = (wave * QS + q) % (SROWS / 64) * 64 + lane;
-    ssrc[q] = C8 && p < TM ? a.xs + (int64_t)min(m0 + p, a.M - 1) * a.kb
-                           : a.ws + (int64_t)(ROWS ? w_row(p - SOFF) : w_row(p - SOFF) >> 7) * a.kb;
+    const int p = (wave * QS + q) % SL * 64 + lane;
+    soff[q] = (uint32_t)(C8 && p < TM ? p : p - SOFF) * (uint32_t)a.kb * 4;
   }
-  auto place = [&](uint8_t* to, int q) { return to + (q < QA ? (wave * QA + q) * 1024 : TM * XB + (wave * QB + q - QA) * 1024); };
-  // stage `it` into place `to`; past the last one the last again, into a place that is not read any more
-  auto issue = [&](int it, uint8_t* to) {
-    it = min(it, stages - 1);
-    const bool whole = (it + 1) * 128 <= a.K;
+  typedef const float __attribute__((address_space(4)))* Scalars;
+  Scalars wsp[NI];
 #pragma unroll
-    for (int q = 0; q < QD; ++q) {
-      const int per = q < QA ? XB : 128;
-      const char* p = src[q] + (int64_t)it * per;
-      if (!whole && it * per + at[q] >= a.K * (per / 128)) p = reinterpret_cast<const char*>(&f8_zeros);
-      __builtin_amdgcn_global_load_lds((gptr)p, (lptr)place(to, q), 16, 0, 0);
+  for (int j = 0; j < NI; ++j) {
+    const int q = wn * NI + j;
+    const int row = MODE == PRODUCT ? min(n0 + q * 16, a.w_rows - 1) : (q & 1) * a.F + min(n0 + (q >> 1) * 16, a.F - 1);
+    wsp[j] = (Scalars)(a.ws + (int64_t)(row >> 7) * a.kb);
+  }
+  // load q of stage `it` into place `to`; past the last stage into a place that is not read any more
+  auto issue = [&](int it, uint8_t* to, int q) {
+    const int left = a.K - it * 128;       // of K, for the pieces that lie past it
+    if (q < QA) {
+      const int n = wave * QA + q, v = (QA % XV == 0 ? q : n) % XV;
+      const uint32_t at = xpiece[v] * (C8 ? 16 : 8) < left ? xlane + xpiece[v] * 16 : PAST;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (lptr)(to + n * 1024), 16, (int)at, (int)(n * XR * xpitch + it * XB), 0, 0);
+    } else if (q < QD) {
+      const int n = wave * QB + q - QA, v = (QB % 2 == 0 ? q - QA : n) % 2;
+      const int half = MODE == PRODUCT ? 0 : n >> 1 & 1, row = MODE == PRODUCT ? n * 8 : (n >> 2) * 16 + (n & 1) * 8;
+      const uint32_t at = wpiece[v] * 16 < left ? wlane + wpiece[v] * 16 : PAST;
+      const Buffer wb = f8_buffer(half ? wbase + (int64_t)a.F * a.K : wbase, (int64_t)wrows * a.K);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wb, (lptr)(to + TM * XB + n * 1024), 16, (int)at,
+                                               (int)(row * wpitch + it * 128), 0, 0);
+    } else {
+      const int n = (wave * QS + q - QD) % SL;
+      const uint32_t at = left > 0 ? soff[q - QD] : PAST;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(C8 && n * 64 < TM ? xsb : wsb, (lptr)(to + PIECES + n * 256), 4, (int)at, it * 4, 0, 0);
     }
-#pragma unroll
-    for (int q = 0; q < QS; ++q)
-      __builtin_amdgcn_global_load_lds((gptr)(ssrc[q] + it), (lptr)(to + PIECES + (wave * QS + q) % (SROWS / 64) * 256), 4, 0, 0);
   };
   auto barrier = [] {
     asm volatile("" ::: "memory");   // no LDS access moves across it
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
-  // fragments: lane 16 g + r reads pieces 2 g and 2 g + 1 of row r of codes, pieces 4 g .. 4 g + 3 of 16-bit rows
+  // fragments: lane 16 g + r reads pieces g and 4 + g of row r of codes, the same k of 16-bit rows.  (Next to each other
+  // for next g: the 16 lanes whose reads go together are of two g, rows 0 .. 3 and 12 .. 15 of one and 4 .. 11 of the
+  // other or the reverse, and with pieces 2 g and 2 g + 1 they met in half of the banks.)
   int foff[2], xoff[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) foff[h] = r * 128 + (((2 * g + h) ^ (r >> 1 & 7)) * 16);
+  for (int h = 0; h < 2; ++h) foff[h] = r * 128 + (((4 * h + g) ^ (r >> 1 & 7)) * 16);
+  const int xrow = wm * MI * 16 * XB, wrow = TM * XB + wn * NI * 2048;   // the wave's first rows in a stage
 #pragma unroll
-  for (int h = 0; h < 4; ++h) xoff[h] = r * 256 + (((4 * g + h) ^ r) * 16);
+  for (int q = 0; q < 4; ++q) xoff[q] = r * 256 + (((8 * (q >> 1) + 2 * g + (q & 1)) ^ r) * 16);
+  typedef std::conditional_t<ROWS, f4, float> F;
+  // The last row of blocks goes through its blocks from HALF on and around: the fragments of the others, which it needs
+  // last, have a second place (`other`), the later ones are read again as soon as it has used them.
+  constexpr int HALF = NI / 2;
+  auto block = [](int i, int s) { return i == MI - 1 ? (s + HALF) % NI : s; };   // the block in turn s of row i
+  u4 first[HALF][2], late[HALF][2], other[HALF][2];
+  F ws[NI], ws_next[NI];   // W's scales
+  // `at`: a stage's place in smem.  It is kept from the compiler where one lies (opaque()): it would hold every
+  // fragment's address in a register of its own.
+  auto opaque = [](int at) {
+    asm volatile("" : "+s"(at));
+    return at;
+  };
+  auto read_w = [&](int at, int j, u4 (&to)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) to[h] = *reinterpret_cast<const u4*>(smem + (at + wrow + foff[h]) + j * 2048);
+  };
+  auto read_ws = [&](int at, int it, F (&to)[NI]) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      if constexpr (ROWS) to[j] = *reinterpret_cast<const f4*>(smem + (at + PIECES + (SOFF + wn * NI * 16 + 4 * g) * 4) + j * 64);
+      else to[j] = wsp[j][min(it, stages - 1)];
+    }
+  };
+  u4 x[2][C8 ? 2 : 4];
+  float sx[2] = {1.f, 1.f};
+  auto read_x = [&](int at, int i) {
+#pragma unroll
+    for (int h = 0; h < (C8 ? 2 : 4); ++h)
+      x[i & 1][h] = *reinterpret_cast<const u4*>(smem + (at + xrow + (C8 ? foff[h & 1] : xoff[h])) + i * (16 * XB));
+    if constexpr (C8) sx[i & 1] = *reinterpret_cast<const float*>(smem + (at + PIECES + (wm * MI * 16 + r) * 4) + i * 64);
+  };
   f4 acc[MI][NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+  // A block's products join its sum LAG blocks later: the matrix cores' results take their time to come.  part, f:
+  // the outstanding blocks' products and factors.
+  constexpr int LAG = FAST ? 3 : NI, KEPT = FAST ? 4 : NI;
+  static_assert(MI * NI % KEPT == 0, "the next stage's first block takes place 0 again");
+  f4 part[KEPT];
+  F f[KEPT];
+#pragma unroll
+  for (int t = 0; t < KEPT; ++t) {
+    part[t] = f4{0.f, 0.f, 0.f, 0.f};
+    f[t] = F{};
+  }
+  auto join = [&](int t) {   // block t (counted along the rows of blocks), t < 0: of the stage before
+    const int at = (t + MI * NI) % (MI * NI), p = at % KEPT, i = at / NI, j = block(i, at % NI);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (ROWS) acc[i][j][k] = fmaf(part[p][k], f[p][k], acc[i][j][k]);
+      else acc[i][j][k] = fmaf(part[p][k], f[p], acc[i][j][k]);
+    }
+  };
 
 #pragma unroll
-  for (int it = 0; it < RING - 1; ++it) issue(it, smem + it * STAGE);
-  int cur = 0, fill = RING - 1;
-#pragma unroll 1
-  for (int it = 0; it < stages; ++it) {
-    wait_loads<(RING - 2) * (QD + QS)>();
-    barrier();
-    issue(it + RING - 1, smem + fill * STAGE);
-    fill = fill + 1 == RING ? 0 : fill + 1;
-    const uint8_t* const st = smem + cur * STAGE;
-    const float* const sc = reinterpret_cast<const float*>(st + PIECES);
-    cur = cur + 1 == RING ? 0 : cur + 1;
-    u4 b[NI][2];
-    f4 sw[NI];
+  for (int it = 0; it < RING; ++it)
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int row = (wn * NI + j) * 16;
+    for (int q = 0; q < QALL; ++q) issue(it, smem + it * STAGE, q);
+  wait_loads<(RING - 1) * QALL>();
+  barrier();
+  int cur = opaque(0);   // the place of the stage at hand
+  read_x(cur, 0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) b[j][h] = *reinterpret_cast<const u4*>(st + TM * XB + row * 128 + foff[h]);
-      if constexpr (ROWS) sw[j] = *reinterpret_cast<const f4*>(sc + SOFF + row + 4 * g);
-      else sw[j].x = sc[SOFF + row];
+  for (int j = 0; j < NI; ++j) read_w(cur, j, j < HALF ? first[j] : late[j - HALF]);
+  read_ws(cur, 0, ws);
+  // early: the fragments of the first HALF blocks, late: those of the others; next: where the next stage's first ones go
+  auto stage = [&](int it, u4 (&early)[HALF][2], u4 (&late)[HALF][2], u4 (&next)[HALF][2], F (&s)[NI], F (&s_next)[NI]) {
+    const int nxt = opaque(cur == (RING - 1) * STAGE ? 0 : cur + STAGE);
+    auto w = [&](int j) -> u4 (&)[2] { return j < HALF ? early[j] : late[j - HALF]; };
+    u4 half[FAST ? 1 : NI][4];
+    if constexpr (!FAST) {
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) half[j][q] = f8_to_16<XT>(w(j)[q >> 1][2 * (q & 1)], w(j)[q >> 1][2 * (q & 1) + 1]);
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const int row = (wm * MI + i) * 16;
-      u4 x[C8 ? 2 : 4];
+      if (i + 1 < MI) {
+        read_x(cur, i + 1);
+      } else {
+        wait_loads<(RING - 2) * QALL>();
+        barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        read_x(nxt, 0);
 #pragma unroll
-      for (int h = 0; h < (C8 ? 2 : 4); ++h)
-        x[h] = *reinterpret_cast<const u4*>(st + row * XB + (C8 ? foff[h & 1] : xoff[h]));
-      const float sx = C8 ? sc[row + r] : 1.f;
-#pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        f4 part = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (FAST) {
-          part = mfma_f8(b[j][0], b[j][1], x[0], x[1]);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            part = mfma_16<XT>(b[j][q >> 1][2 * (q & 1)], b[j][q >> 1][2 * (q & 1) + 1],
-                               C8 ? u4{x[q >> 1][2 * (q & 1)], x[q >> 1][2 * (q & 1) + 1], 0, 0} : x[q], part);
-        }
-        if constexpr (ROWS) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(part[k], sx * sw[j][k], acc[i][j][k]);
-        } else {
-          const float f = C8 ? sx * sw[j].x : sw[j].x;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[i][j][k] = fmaf(part[k], f, acc[i][j][k]);
-        }
+        for (int j = 0; j < HALF; ++j) read_w(nxt, j, next[j]);
+        read_ws(nxt, it + 1, s_next);
       }
+      u4 xh[4];
+      if constexpr (!FAST) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) xh[q] = C8 ? f8_to_16<XT>(x[i & 1][q >> 1 & 1][2 * (q & 1)], x[i & 1][q >> 1 & 1][2 * (q & 1) + 1]) : x[i & 1][C8 ? 0 : q];
+      }
+      constexpr int Q = FAST ? 1 : 4;
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int n = 0; n < NI; ++n) {
+          const int t = i * NI + n, p = t % KEPT, j = block(i, n);
+          if constexpr (FAST) {
+            part[p] = mfma_f8(w(j)[0], w(j)[1], x[i & 1][0], x[i & 1][1]);
+            join(t - LAG);
+          } else {
+            if (q == 0) join(t - LAG);
+            part[p] = mfma_16<XT>(half[j][q], xh[q], q ? part[p] : f4{0.f, 0.f, 0.f, 0.f});
+          }
+          if (q == 0) f[p] = sx[i & 1] * s[j];
+          if (i == MI - 1 && q == Q - 1) {   // the loads spread over the row
+#pragma unroll
+            for (int l = 0; l < QALL; ++l)
+              if (l * NI / QALL == n) issue(it + RING, smem + cur, l);
+            if (j >= HALF) read_w(nxt, j, late[j - HALF]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
     }
+    cur = nxt;
+  };
+  int it = 0;
+#pragma unroll 1
+  for (; it + 1 < stages; it += 2) {
+    stage(it, first, late, other, ws, ws_next);
+    stage(it + 1, other, late, first, ws_next, ws);
   }
+  if (it < stages) stage(it, first, late, other, ws, ws_next);
+#pragma unroll
+  for (int t = MI * NI - LAG; t < MI * NI; ++t) join(t - MI * NI);
   wait_loads<0>();   // nothing is on its way to LDS any more
   barrier();
   uint8_t* const strip = smem + wave * (16 * (16 * NI + 4) * 4);
@@ -730,19 +827,20 @@ struct F8Plan { int tile, nw; int64_t workgroups; bool fits; };
 enum { KIND_16 = 0, KIND_EXACT = 1, KIND_FAST = 2 };
 struct F8Tile { int rows, cols, threads; };
 constexpr F8Tile F8_TILES[3][3] = {{{64, 64, 256}, {128, 128, 512}, {128, 256, 512}},
-                                   {{64, 64, 256}, {128, 128, 512}, {256, 256, 512}},
+                                   {{64, 64, 256}, {128, 128, 512}, {128, 256, 512}},
                                    {{64, 64, 256}, {128, 128, 256}, {256, 256, 512}}};
 
 int64_t f8_grid(int M, int64_t w_rows, const F8Tile& t) {
   return (((int64_t)M + t.rows - 1) / t.rows * ((w_rows + t.cols - 1) / t.cols) + 7) / 8 * 8;
 }
 
-// N: columns of y, or features of a gated form.
-F8Plan plan_f8(int mode, int M, int N, int K, int kind) {
+// N: columns of y, or features of a gated form.  pitch: bytes from one row of x to the next.
+F8Plan plan_f8(int mode, int M, int N, int K, int64_t pitch, int kind) {
   F8Plan p = {0, 1, 0, true};
   if (M == 0 || N == 0) return p;
   const int64_t chunks = ((int64_t)K + 511) / 512, w_rows = mode == PRODUCT ? N : 2 * (int64_t)N;
-  if (K > 0) {
+  // The tiles' buffers hold 256 rows of codes, or 128 of 16-bit x, in less than 2^31 bytes.  A larger pitch is the rows kernel's.
+  if (K > 0 && pitch <= (1 << 22)) {
     if (M > 16) p.tile = 1;
     if (M > 64 && (int64_t)M * w_rows >= 128 * 128 * 256) p.tile = 2;
     if (M > 128 && (int64_t)M * w_rows >= 256 * 256 * 200) p.tile = 3;
@@ -800,7 +898,7 @@ template <int XT, bool FAST, int MODE, bool ROWS> void launch_f8(const F8Args& a
     if (p.tile == 3) return launch_tiles<XT, FAST, MODE, ROWS, 8, 4, 2, 4, 2>(a, s);
   } else {
     if (p.tile == 2) return launch_tiles<XT, FAST, MODE, ROWS, 4, 2, 2, 4, XT == F8 ? 4 : 3>(a, s);
-    if (p.tile == 3) return launch_tiles<XT, FAST, MODE, ROWS, XT == F8 ? 8 : 4, 4, 2, 4, 2>(a, s);
+    if (p.tile == 3) return launch_tiles<XT, FAST, MODE, ROWS, 4, 4, 2, 4, XT == F8 ? 3 : 2>(a, s);
   }
   if constexpr (!FAST) {
     if (p.nw == 1) return launch_rows<XT, MODE, 1, ROWS>(a, s);
@@ -813,7 +911,7 @@ template <int XT, bool FAST, int MODE, bool ROWS> void launch_f8(const F8Args& a
 
 template <int MODE> int run_f8(const F8Args& a, int x_type, int w_block, void* stream) {
   const int kind = x_type != F8 ? KIND_16 : a.y_type == BF16 && w_block == 128 ? KIND_FAST : KIND_EXACT;
-  const F8Plan p = plan_f8(MODE, a.M, MODE == PRODUCT ? a.N : a.F, a.K, kind);
+  const F8Plan p = plan_f8(MODE, a.M, MODE == PRODUCT ? a.N : a.F, a.K, a.ldx_bytes, kind);
   if (!p.fits) return QG_E_UNSUPPORTED;
   int st = device_present();
   if (st != QG_OK) return st;
