@@ -66,6 +66,7 @@ _SIGS = {
     "qmx_gemm_grouped": ([_P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _I, _I, _P, _I, _I, _P], _I),
     "qmx_plan": ([_I, _I, _I, _I, _I, ctypes.POINTER(_I)], _I),
     "qf8_quantize": ([_P, _I, _I, _I, _I, _I, _I, _P, _P, _P], _I),
+    "qf8_dequantize": ([_P, _P, _I, _I, _I, _P, _I, _I, _P], _I),
     "qf8_gemm": ([_P, _I, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _P, _I, _I, _P], _I),
     "qf8_gated": ([_P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P], _I),
     "qf8_gated_grad": ([_P, _I, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P], _I),
@@ -776,6 +777,27 @@ def f8_quantize(x, block=1, transpose=False, codes=None, scales=None, stream=Non
     if st:
         raise QGemmError(st, "qf8_quantize")
     return codes, scales
+
+
+def f8_dequantize(codes, scales, dtype=torch.float16, out=None, stream=None):
+    """The values of a matrix of E4M3 codes [M, K] and scales (blocks of 1 or 128
+    rows by their shape) as [M, K] of `dtype` (fp16, bf16 or fp32), or into `out`
+    (whose type counts then); see qf8_dequantize."""
+    ctx = _mx_elsewhere(codes, stream)
+    if ctx is not None:
+        with ctx:
+            return f8_dequantize(codes, scales, dtype, out)
+    dev = codes.get_device()
+    M, K, block = _f8_matrix(codes, scales, "codes and scales", dev)
+    if out is None:
+        if dtype not in _MX_TYPE:
+            raise ValueError(f"dtype must be one of {', '.join(str(d) for d in _MX_TYPE)}")
+        out = codes.new_empty((M, K), dtype=dtype)
+    yt, ldy = _mx_float(out, "out", dev, (M, K))
+    st = _lib.qf8_dequantize(codes.data_ptr(), scales.data_ptr(), block, M, K, out.data_ptr(), ldy, yt, _mx_stream(dev))
+    if st:
+        raise QGemmError(st, "qf8_dequantize")
+    return out
 
 
 def f8_gemm(x, w, w_scales, x_scales=None, out=None, out_dtype=None, residual=None, stream=None):

@@ -81,6 +81,11 @@ template <int T> __device__ __forceinline__ void load8_or_zero(const typename El
   if (have) load8<T>(p, v);
 }
 
+// i / per, for i below n: in 32 bits where they hold it (a 64-bit division takes as long as a block's conversion).
+__device__ __forceinline__ int64_t row_of(int64_t i, uint32_t per, int64_t n) {
+  return n <= (int64_t)UINT32_MAX ? (int64_t)((uint32_t)i / per) : i / per;
+}
+
 // Blocks of 128 along a row: a lane takes 8 elements, 16 lanes a block (the
 // last block of a row may have idle ones), so a wave's codes are 512 contiguous
 // bytes.  n: 16-lane groups, kb of them a row.
@@ -92,7 +97,7 @@ __global__ __launch_bounds__(EW_THREADS) void f8_quantize_rows_kernel(const type
   const int64_t step = (int64_t)gridDim.x * (EW_THREADS / 16);
   const int lane = threadIdx.x & 15;
   for (int64_t i = (int64_t)blockIdx.x * (EW_THREADS / 16) + (threadIdx.x >> 4); i < n; i += step) {
-    const int64_t r = i / kb;
+    const int64_t r = row_of(i, kb, n);
     const int k = (int)(i - r * kb) * 128 + lane * 8;
     float v[8];
     load8_or_zero<T>(x + r * ldx + k, k < K, v);
@@ -106,6 +111,36 @@ __global__ __launch_bounds__(EW_THREADS) void f8_quantize_rows_kernel(const type
     const u2 c = {f8_codes(v[0], v[1], v[2], v[3]), f8_codes(v[4], v[5], v[6], v[7])};
     if (k < K) *reinterpret_cast<u2*>(codes + r * K + k) = b.finite ? c : u2{0, 0};
     if (lane == 0) scales[i] = f8_scale(top);
+  }
+}
+
+// Reading back, 16 bytes of y a lane (4 codes for fp32, 8 for 16 bits): each value rounded once.  n: such groups,
+// per of them a row; shift 0 or 7: rows of a block.  Bound by HBM.
+template <int T>
+__global__ __launch_bounds__(EW_THREADS) void f8_dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                                   const float* __restrict__ scales, int shift, int kb,
+                                                                   uint32_t per, int64_t n,
+                                                                   typename Elem<T>::type* __restrict__ y, int64_t ldy) {
+  typedef typename Elem<T>::type E;
+  constexpr int C = 16 / sizeof(E);
+  typedef E Out __attribute__((ext_vector_type(C)));
+  const int64_t step = (int64_t)gridDim.x * EW_THREADS;
+  for (int64_t i = (int64_t)blockIdx.x * EW_THREADS + threadIdx.x; i < n; i += step) {
+    const int64_t r = row_of(i, per, n);
+    const uint32_t k = (uint32_t)(i - r * per) * C;
+    const float s = scales[(r >> shift) * kb + (k >> 7)];
+    const uint32_t* from = reinterpret_cast<const uint32_t*>(codes) + i * (C / 4);
+    Out v;
+#pragma unroll
+    for (int j = 0; j < C / 4; ++j) {
+      const uint32_t w = from[j];
+      const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+      v[4 * j] = (E)(a.x * s);
+      v[4 * j + 1] = (E)(a.y * s);
+      v[4 * j + 2] = (E)(b.x * s);
+      v[4 * j + 3] = (E)(b.y * s);
+    }
+    *reinterpret_cast<Out*>(y + r * ldy + k) = v;
   }
 }
 
@@ -1003,6 +1038,32 @@ extern "C" int qf8_quantize(const void* x, int ldx, int x_type, int M, int K, in
   if (x_type == F16) launch_quantize<F16>(x, ldx, M, K, block, transpose, codes, scales, s);
   else if (x_type == BF16) launch_quantize<BF16>(x, ldx, M, K, block, transpose, codes, scales, s);
   else launch_quantize<F32>(x, ldx, M, K, block, transpose, codes, scales, s);
+  return launch_status();
+}
+
+extern "C" int qf8_dequantize(const uint8_t* codes, const float* scales, int block, int M, int K, void* y, int ldy,
+                              int y_type, void* stream) {
+  if (!float_type(y_type) || M < 0 || K < 0 || K % 16 || (block != 1 && block != 128)) return QG_E_ARG;
+  if (M == 0 || K == 0) return QG_OK;
+  if (!y || !codes || !scales || ldy < K) return QG_E_ARG;
+  if (!aligned(y, 16) || !aligned(codes, 16) || !aligned(scales, 4) || ldy % 8) return QG_E_ALIGN;
+  int st = device_present();
+  if (st != QG_OK) return st;
+  const void* ptrs[3] = {codes, scales, y};
+  st = check_device_pointers(ptrs, 3);
+  if (st != QG_OK) return st;
+  clear_pending_error();
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const uint32_t per = y_type == F32 ? K / 4 : K / 8;
+  const int64_t n = (int64_t)M * per;
+  const int shift = block == 1 ? 0 : 7, kb = (int)(((int64_t)K + 127) / 128);
+  const dim3 grid((unsigned)std::min<int64_t>((n + EW_THREADS - 1) / EW_THREADS, 256 * 16)), threads(EW_THREADS);
+  if (y_type == F16)
+    hipLaunchKernelGGL(f8_dequantize_kernel<F16>, grid, threads, 0, s, codes, scales, shift, kb, per, n, reinterpret_cast<f16*>(y), (int64_t)ldy);
+  else if (y_type == BF16)
+    hipLaunchKernelGGL(f8_dequantize_kernel<BF16>, grid, threads, 0, s, codes, scales, shift, kb, per, n, reinterpret_cast<bf16*>(y), (int64_t)ldy);
+  else
+    hipLaunchKernelGGL(f8_dequantize_kernel<F32>, grid, threads, 0, s, codes, scales, shift, kb, per, n, reinterpret_cast<float*>(y), (int64_t)ldy);
   return launch_status();
 }
 

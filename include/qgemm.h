@@ -451,6 +451,15 @@ int qf8_quantize(const void* x, int ldx, int x_type, int M, int K, int block, in
                  float* scales, void* stream);
 
 /*
+ * qf8_dequantize: codes [M, K] and scales in blocks of `block` (1 or 128) -> y [M, K] of y_type
+ * QG_MX_F16, QG_MX_BF16 or QG_MX_F32, leading dimension ldy >= K, ldy % 8 == 0: code times scale in
+ * fp32, rounded once more to 16 bits.
+ * M == 0 or K == 0 is a no-op.  Errors: QG_E_ARG, QG_E_ALIGN, QG_E_DEVICE, QG_E_NOT_DEVICE.
+ */
+int qf8_dequantize(const uint8_t* codes, const float* scales, int block, int M, int K, void* y, int ldy, int y_type,
+                   void* stream);
+
+/*
  * qf8_gemm: y[M, N] = x[M, K] . W[N, K]^T (+ residual), W in E4M3.  The codes'
  * products are summed in fp32 over a block of 128 k, the blocks' sums times
  * their scales in fp32; one rounding to y_type at the end.

@@ -126,6 +126,10 @@ def quantize(x=A, ldx=None, xt=F16, M=2, K=64, block=1, turn=0, codes=A, scales=
     return lib.qf8_quantize(x, K if ldx is None else ldx, xt, M, K, block, turn, codes, scales, None)
 
 
+def dequantize(codes=A, scales=A, block=1, M=2, K=64, y=A, ldy=None, yt=F16):
+    return lib.qf8_dequantize(codes, scales, block, M, K, y, K if ldy is None else ldy, yt, None)
+
+
 def gemm(x=A, ldx=None, xt=F16, xs=None, w=A, ws=A, block=128, res=None, ldr=None, M=2, N=16, K=64, y=A, ldy=None, yt=F16):
     return lib.qf8_gemm(x, K if ldx is None else ldx, xt, xs, w, ws, block, res, N if ldr is None else ldr, M, N, K, y,
                         N if ldy is None else ldy, yt, None)
@@ -150,6 +154,15 @@ def grad(dh=A, ldd=None, x=A, ldx=None, xt=F16, xs=None, w=A, ws=A, act=0, M=2, 
     (dict(M=0, x=None), OK), (dict(K=0, codes=None), OK)])
 def test_quantize_refuses(kw, expect):
     assert quantize(**kw) == expect
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(yt=FP4), E_ARG), (dict(yt=F8), E_ARG), (dict(M=-1), E_ARG), (dict(K=-16), E_ARG), (dict(K=24), E_ARG),
+    (dict(block=2), E_ARG), (dict(y=None), E_ARG), (dict(codes=None), E_ARG), (dict(scales=None), E_ARG),
+    (dict(ldy=48), E_ARG), (dict(y=A + 2), E_ALIGN), (dict(codes=A + 8), E_ALIGN), (dict(scales=A + 2), E_ALIGN),
+    (dict(ldy=68), E_ALIGN), (dict(M=0, y=None), OK), (dict(K=0, codes=None), OK)])
+def test_dequantize_refuses(kw, expect):
+    assert dequantize(**kw) == expect
 
 
 PRODUCT_REFUSALS = [
@@ -185,7 +198,7 @@ def test_grad_refuses(kw, expect):
 
 @pytest.mark.skipif(gpu_present(), reason="checks the no-device status; a GPU is present")
 def test_no_device_status():
-    assert quantize() == E_DEVICE and quantize(block=128, turn=1) == E_DEVICE
+    assert quantize() == E_DEVICE and quantize(block=128, turn=1) == E_DEVICE and dequantize() == E_DEVICE
     assert gemm() == E_DEVICE and gemm(xt=F8, xs=A + 4, block=1) == E_DEVICE and gemm(K=0, x=None, w=None) == E_DEVICE
     assert gated() == E_DEVICE and gated(act=1, xt=F8, xs=A) == E_DEVICE and grad() == E_DEVICE
 
@@ -220,6 +233,7 @@ def test_binding_refuses_sizes_and_strides_past_32_bits(no_library):
     few, far, many = meta((2, 64)), meta((2, 64), stride=(big + 64, 1)), meta((big + 2, 64))
     w, ws = f8(64, 64)
     for call in (lambda: qgm.f8_quantize(far), lambda: qgm.f8_quantize(many), lambda: qgm.f8_quantize(meta((1, big + 64))),
+                 lambda: qgm.f8_dequantize(*f8(2, 64), out=far), lambda: qgm.f8_dequantize(*f8(big + 2, 64)),
                  lambda: qgm.f8_gemm(far, w, ws), lambda: qgm.f8_gemm(many, w, ws), lambda: qgm.f8_gemm(few, w, ws, out=far),
                  lambda: qgm.f8_gemm(few, w, ws, residual=far), lambda: qgm.f8_gemm(few, *f8(big + 3, 64)),
                  lambda: qgm.f8_gemm(meta((1, big + 64)), *f8(3, big + 64)),
@@ -239,6 +253,8 @@ def test_binding_refuses_what_does_not_fit(no_library):
     for call in (lambda: qgm.f8_quantize(meta((2, 40))), lambda: qgm.f8_quantize(x, block=64), lambda: qgm.f8_quantize(c),
                  lambda: qgm.f8_quantize(meta((2, 64), stride=(1, 2))), lambda: qgm.f8_quantize(x, codes=w),
                  lambda: qgm.f8_quantize(x, scales=ws), lambda: qgm.f8_quantize(x, transpose=True, codes=c),
+                 lambda: qgm.f8_dequantize(c, cs, dtype=torch.float64), lambda: qgm.f8_dequantize(c, cs, out=h),
+                 lambda: qgm.f8_dequantize(c, w1), lambda: qgm.f8_dequantize(x, cs),
                  lambda: qgm.f8_gemm(meta((2, 128)), w, ws), lambda: qgm.f8_gemm(meta((2, 256), torch.float32), w, ws),
                  lambda: qgm.f8_gemm(c, w, ws), lambda: qgm.f8_gemm(c, w, ws, x_scales=cs.t()),
                  lambda: qgm.f8_gemm(x, w, w1), lambda: qgm.f8_gemm(x, w, ws, x_scales=cs),
@@ -260,7 +276,7 @@ def test_binding_refuses_what_does_not_fit(no_library):
 def test_binding_refuses_cpu_tensors():
     x = torch.zeros(2, 64, dtype=torch.float16)
     c, s = torch.zeros(32, 64, dtype=torch.float8_e4m3fn), torch.zeros(1, 1)
-    for call in (lambda: qgm.f8_quantize(x), lambda: qgm.f8_gemm(x, c, s), lambda: qgm.f8_gated(x, c, s),
+    for call in (lambda: qgm.f8_quantize(x), lambda: qgm.f8_dequantize(c, s), lambda: qgm.f8_gemm(x, c, s), lambda: qgm.f8_gated(x, c, s),
                  lambda: qgm.f8_gated_grad(x[:, :16], x, c, s), lambda: qgm.F8Linear(c, s), lambda: qgm.F8Gated(c, s),
                  lambda: qgm.F8Linear.from_weight(x), lambda: qgm.F8Gated.from_weight(x)):
         with pytest.raises(ValueError, match="GPU"):

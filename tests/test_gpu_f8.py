@@ -197,10 +197,27 @@ def test_quantize_ends_of_the_range(dtype):
         check_quantize(x, block, transpose)
 
 
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("M,K", [(1, 16), (3, 256), (257, 2064), (1000, 48), (130, 144)])
+def test_dequantize(dtype, block, M, K):
+    # every code, scales of every size; one fp32 rounding, and one to 16 bits
+    rng = np.random.default_rng(M + K)
+    codes = rng.permutation(np.arange(M * K) % 256).astype(np.uint8).reshape(M, K)
+    scales = (rng.uniform(0.5, 2, (-(-M // block), -(-K // 128))) * np.exp2(rng.integers(-12, 6, (-(-M // block), 1)))).astype(np.float32)
+    with np.errstate(over="ignore"):
+        want = rounded(f8ref.f8_values(codes, scales), dtype)
+    out = torch.full((M + 1, K + 16), 5.0, dtype=dtype, device=DEV)
+    for y in (qgm.f8_dequantize(dev(codes), dev(scales), dtype=dtype), qgm.f8_dequantize(dev(codes), dev(scales), out=out[:M, 8:K + 8])):
+        assert np.array_equal(f64(y), want, equal_nan=True)
+    assert bool((out[M] == 5).all()) and bool((out[:, :8] == 5).all()) and bool((out[:, K + 8:] == 5).all())
+
+
 @pytest.mark.parametrize("M,K", [(0, 64), (4, 0)])
 def test_quantize_empty(M, K):
     for block in (1, 128):
         codes, scales = qgm.f8_quantize(torch.zeros(M, K, dtype=F16, device=DEV), block=block)
+        assert qgm.f8_dequantize(codes, scales).shape == (M, K)
         assert codes.shape == (M, K) and scales.shape == (M if block == 1 else -(-M // 128), -(-K // 128))
         codes, scales = qgm.f8_quantize(torch.zeros(M, K, dtype=F16, device=DEV), block=block, transpose=True)
         assert codes.shape == (K, -(-M // 16) * 16)
@@ -215,6 +232,9 @@ def test_quantize_far_offsets():
     codes, scales = qgm.f8_quantize(x)
     assert np.array_equal(codes_of(codes[M - 3:]), want_c) and np.array_equal(scales[M - 3:].cpu().numpy(), want_s)
     assert not bool(codes[:M - 3].view(torch.uint8).any())
+    back = qgm.f8_dequantize(codes, scales, dtype=F32)      # 17 GiB
+    assert np.array_equal(f64(back[M - 3:]), rounded(f8ref.f8_values(want_c, want_s), F32)) and not bool(back[:M - 3].any())
+    del back
     tail = x[M - M % 128:, K - 16:]
     want_c, want_s = f8ref.f8_quantize(f64(tail), transpose=True)
     codes, scales = qgm.f8_quantize(x, transpose=True)
