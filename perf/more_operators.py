@@ -224,7 +224,7 @@ def _own(s):
     case = s["case"]
     if case["op"] == "quantise":
         codes, scales = qg.f8_quantize(s["x"], block=case["block"], transpose=case["transpose"])
-        return _values(codes, scales, case["block"]), scales
+        return qg.f8_dequantize(codes, scales, dtype=torch.float32), scales
     yt = TYPES[case["yt"]]
     if case["op"] == "product":
         return qg.f8_gemm(s["x"], s["w"], s["ws"], x_scales=s["xs"], residual=s["residual"], out_dtype=yt)
