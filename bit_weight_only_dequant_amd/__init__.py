@@ -70,6 +70,7 @@ _SIGS = {
     "qf8_gemm": ([_P, _I, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _P, _I, _I, _P], _I),
     "qf8_gated": ([_P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P], _I),
     "qf8_gated_grad": ([_P, _I, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P], _I),
+    "qf8_plan": ([_I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_I)], _I),
     "qg_stream_read": ([_P, _SZ, _P, _I, _P], _I),
     "qg_empty_launch": ([_I, _I, _P], _I),
     "qg_mfma_probe": ([_P, _I, _I, _P], _I),
@@ -871,6 +872,14 @@ def f8_gated_grad(dh, x, w, w_scales, x_scales=None, act="silu", out=None, strea
     if st:
         raise QGemmError(st, "qf8_gated_grad")
     return out
+
+
+def f8_plan(M: int, N: int, K: int, x_type: int, y_type: int = MX_BF16, w_block: int = 128, gated: bool = False) -> dict:
+    """The kernel a product of 8-bit weights takes; see qf8_plan."""
+    out = (_I * 3)()
+    _mx_int("plan", M, N, K)
+    _check(_lib.qf8_plan(1 if gated else 0, M, N, K, x_type, y_type, w_block, out), "qf8_plan")
+    return dict(tile=out[0], waves=out[1], pieces=out[2])
 
 
 class F8Linear:

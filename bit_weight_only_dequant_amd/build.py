@@ -7,6 +7,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -30,15 +31,15 @@ def build(verbose: bool = True) -> str:
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     out_dir = os.path.join(PKG, "_build")
     os.makedirs(out_dir, exist_ok=True)
-    host_o = os.path.join(out_dir, "host.o")
-    # host-only translation unit (no device code, no device flags)
-    _run([hipcc, *COMMON, "-c", os.path.join(CSRC, "host.cpp"), "-o", host_o], verbose)
-    objs = [host_o]
-    for src in sorted(f for f in os.listdir(CSRC) if f.endswith(".hip")):
-        obj = os.path.join(out_dir, src[:-4] + ".o")
-        _run([hipcc, *COMMON, f"--offload-arch={ARCH}", *DEVICE_FLAGS, "-c",
-              os.path.join(CSRC, src), "-o", obj], verbose)
+    # host.cpp is host-only (no device code, no device flags); the sources are compiled side by side
+    device = [f"--offload-arch={ARCH}", *DEVICE_FLAGS]
+    cmds, objs = [], []
+    for src in ["host.cpp"] + sorted(f for f in os.listdir(CSRC) if f.endswith(".hip")):
+        obj = os.path.join(out_dir, os.path.splitext(src)[0] + ".o")
+        cmds.append([hipcc, *COMMON, *(device if src.endswith(".hip") else []), "-c", os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)
+    with ThreadPoolExecutor(4) as pool:
+        list(pool.map(lambda cmd: _run(cmd, verbose), cmds))
     tmp = LIB + ".tmp"
     _run([hipcc, "-shared", f"--offload-arch={ARCH}", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB)

@@ -615,9 +615,13 @@ constexpr uint32_t PAST = 0x80000000u;   // an offset past every buffer's end
 // that this one has been read: the next fragments of W and the first of x are
 // read, and the loads of stage it + RING sent for, while that row is multiplied.
 // FAST: 8-bit matrix instructions; else the codes are converted to 16 bits.
+// KG: so many groups of WM x WN waves share a tile, group g taking every KG-th
+// stage from the gth on in a ring of its own; their sums are added through LDS in
+// the groups' order.  (A stage of a small tile is a chain of waits that a single
+// group of waves cannot fill.)
 // W is the first operand: a lane's outputs run along a row of y.
-template <int XT, bool FAST, int MODE, bool ROWS, int MI, int NI, int WM, int WN, int RING>
-__global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args a, int tiles_m, int tiles_n) {
+template <int XT, bool FAST, int MODE, bool ROWS, int MI, int NI, int WM, int WN, int RING, int KG>
+__global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_eu(2))) void f8_tile_kernel(F8Args a, int tiles_m, int tiles_n) {
   constexpr int NW = WM * WN, TM = 16 * MI * WM, TN = 16 * NI * WN, TF = MODE == PRODUCT ? TN : TN / 2;
   constexpr bool C8 = XT == F8;
   constexpr int XB = C8 ? 128 : 256, XR = 1024 / XB;         // bytes of an x row a stage, rows a direct load brings
@@ -629,16 +633,18 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args a, int til
   static_assert(SROWS % 64 == 0 && SOFF % 64 == 0, "a load brings the scales of 64 rows, of x or of W");
   constexpr int SL = SROWS / 64 > 0 ? SROWS / 64 : 1, QS = (SROWS / 64 + NW - 1) / NW, QALL = QD + QS;   // such loads, and a wave's
   constexpr int PIECES = TM * XB + TN * 128, STAGE = PIECES + SROWS * 4;
-  static_assert(NW * 16 * (16 * NI + 4) * 4 <= RING * STAGE, "the strips of f8_store_as");
+  static_assert(NW * 16 * (16 * NI + 4) * 4 <= RING * STAGE && (KG == 1 || 16 * (16 * NI + 4) <= MI * NI * 256),
+                "the strips of f8_store_as: a wave's lies within its own part of the sums");
   // one array: with two, the compiler waits for every direct load before each read
-  __shared__ __align__(1024) uint8_t smem[RING * STAGE];
+  __shared__ __align__(1024) uint8_t smem[KG * RING * STAGE];
   int tm, tn;
   if (!f8_tile(tiles_m, tiles_n, tm, tn)) return;
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 6) / NW;   // the wave's group, and its number there
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) - kg * NW;
   const int wm = wave / WN, wn = wave % WN;
   const int m0 = tm * TM, n0 = tn * TF;                       // n0: first column, or feature
-  const int stages = a.kb;
+  const int stages = (a.kb + KG - 1) / KG;                    // of a group; stage `it` of it is block KG it + kg of K
   const uint32_t xpitch = (uint32_t)a.ldx_bytes, wpitch = (uint32_t)a.K;
 
   // The tile's rows as buffers (the host sees to it that a tile's rows stay below 2^31 bytes).  Row p of the
@@ -675,8 +681,9 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args a, int til
     const int row = MODE == PRODUCT ? min(n0 + q * 16, a.w_rows - 1) : (q & 1) * a.F + min(n0 + (q >> 1) * 16, a.F - 1);
     wsp[j] = (Scalars)(a.ws + (int64_t)(row >> 7) * a.kb);
   }
-  // load q of stage `it` into place `to`; past the last stage into a place that is not read any more
+  // load q of stage `it` into place `to`; past K zeros
   auto issue = [&](int it, uint8_t* to, int q) {
+    it = it * KG + kg;
     const int left = a.K - it * 128;       // of K, for the pieces that lie past it
     if (q < QA) {
       const int n = wave * QA + q, v = (QA % XV == 0 ? q : n) % XV;
@@ -710,10 +717,13 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args a, int til
 #pragma unroll
   for (int q = 0; q < 4; ++q) xoff[q] = r * 256 + (((8 * (q >> 1) + 2 * g + (q & 1)) ^ r) * 16);
   typedef std::conditional_t<ROWS, f4, float> F;
-  // The last row of blocks goes through its blocks from HALF on and around: the fragments of the others, which it needs
-  // last, have a second place (`other`), the later ones are read again as soon as it has used them.
+  // Two ways to have the fragments in time.  WHOLE: a stage's are all read while the one before is multiplied, where
+  // registers hold two stages' of them.  Else x is read one row of blocks ahead, and the last row goes through its
+  // blocks from HALF on and around: the fragments of the others, which it needs last, have a second place (`other`),
+  // the later ones are read again as soon as it has used them.
+  constexpr bool WHOLE = MI * NI <= (FAST ? 16 : 8);
   constexpr int HALF = NI / 2;
-  auto block = [](int i, int s) { return i == MI - 1 ? (s + HALF) % NI : s; };   // the block in turn s of row i
+  auto block = [](int i, int s) { return !WHOLE && i == MI - 1 ? (s + HALF) % NI : s; };   // the block in turn s of row i
   u4 first[HALF][2], late[HALF][2], other[HALF][2];
   F ws[NI], ws_next[NI];   // W's scales
   // `at`: a stage's place in smem.  It is kept from the compiler where one lies (opaque()): it would hold every
@@ -730,7 +740,7 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args a, int til
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       if constexpr (ROWS) to[j] = *reinterpret_cast<const f4*>(smem + (at + PIECES + (SOFF + wn * NI * 16 + 4 * g) * 4) + j * 64);
-      else to[j] = wsp[j][min(it, stages - 1)];
+      else to[j] = wsp[j][min(it * KG + kg, a.kb - 1)];
     }
   };
   u4 x[2][C8 ? 2 : 4];
@@ -769,17 +779,94 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args a, int til
 #pragma unroll
   for (int it = 0; it < RING; ++it)
 #pragma unroll
-    for (int q = 0; q < QALL; ++q) issue(it, smem + it * STAGE, q);
+    for (int q = 0; q < QALL; ++q) issue(it, smem + kg * (RING * STAGE) + it * STAGE, q);
   wait_loads<(RING - 1) * QALL>();
   barrier();
-  int cur = opaque(0);   // the place of the stage at hand
+  const int ring = kg * (RING * STAGE);
+  int cur = opaque(ring);   // the place of the stage at hand
+  if constexpr (WHOLE) {
+    constexpr int XP = C8 ? 2 : 4, READS = MI * XP + NI * 2;
+    struct Frags { u4 x[MI][XP], w[NI][2]; float sx[MI]; F s[NI]; };
+    auto read = [&](int at, Frags& f, int n) {   // read n of a stage's fragments
+      if (n < NI * 2) {
+        const int j = n / 2, h = n % 2;
+        f.w[j][h] = *reinterpret_cast<const u4*>(smem + (at + wrow + foff[h]) + j * 2048);
+      } else {
+        const int i = (n - NI * 2) / XP, h = (n - NI * 2) % XP;
+        f.x[i][h] = *reinterpret_cast<const u4*>(smem + (at + xrow + (C8 ? foff[h & 1] : xoff[h])) + i * (16 * XB));
+        if (h == 0) f.sx[i] = C8 ? *reinterpret_cast<const float*>(smem + (at + PIECES + (wm * MI * 16 + r) * 4) + i * 64) : 1.f;
+      }
+    };
+    auto stage = [&](int it, const Frags& c, Frags& next) {
+      const int nxt = opaque(cur == ring + (RING - 1) * STAGE ? ring : cur + STAGE);
+      wait_loads<(RING - 2) * QALL>();
+      barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      read_ws(nxt, it + 1, next.s);
+      u4 half[FAST ? 1 : NI][4];
+      if constexpr (!FAST) {
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) half[j][q] = f8_to_16<XT>(c.w[j][q >> 1][2 * (q & 1)], c.w[j][q >> 1][2 * (q & 1) + 1]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        u4 xh[4];
+        if constexpr (!FAST) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            xh[q] = C8 ? f8_to_16<XT>(c.x[i][q >> 1 & 1][2 * (q & 1)], c.x[i][q >> 1 & 1][2 * (q & 1) + 1]) : c.x[i][C8 ? 0 : q];
+        }
+        constexpr int Q = FAST ? 1 : 4;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+          for (int j = 0; j < NI; ++j) {
+            const int t = i * NI + j, p = t % KEPT;
+            if constexpr (FAST) {
+              part[p] = mfma_f8(c.w[j][0], c.w[j][1], c.x[i][0], c.x[i][1]);
+              join(t - LAG);
+            } else {
+              if (q == 0) join(t - LAG);
+              part[p] = mfma_16<XT>(half[j][q], xh[q], q ? part[p] : f4{0.f, 0.f, 0.f, 0.f});
+            }
+            if (q == 0) f[p] = c.sx[i] * c.s[j];
+            // the next stage's reads spread over the first half of the products, the loads over all of them: issued at
+            // once they hold the wave up
+            constexpr int SLOTS = MI * NI * Q;
+            const int slot = (i * Q + q) * NI + j;
+#pragma unroll
+            for (int n = 0; n < READS; ++n)
+              if (n * (SLOTS / 2) / READS == slot) read(nxt, next, n);
+#pragma unroll
+            for (int l = 0; l < QALL; ++l)
+              if (l * SLOTS / QALL == slot) issue(it + RING, smem + cur, l);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+      }
+      cur = nxt;
+    };
+    Frags f0, f1;
+#pragma unroll
+    for (int n = 0; n < READS; ++n) read(cur, f0, n);
+    read_ws(cur, 0, f0.s);
+    int it = 0;
+#pragma unroll 1
+    for (; it + 1 < stages; it += 2) {
+      stage(it, f0, f1);
+      stage(it + 1, f1, f0);
+    }
+    if (it < stages) stage(it, f0, f1);
+  } else {
   read_x(cur, 0);
 #pragma unroll
   for (int j = 0; j < NI; ++j) read_w(cur, j, j < HALF ? first[j] : late[j - HALF]);
   read_ws(cur, 0, ws);
   // early: the fragments of the first HALF blocks, late: those of the others; next: where the next stage's first ones go
   auto stage = [&](int it, u4 (&early)[HALF][2], u4 (&late)[HALF][2], u4 (&next)[HALF][2], F (&s)[NI], F (&s_next)[NI]) {
-    const int nxt = opaque(cur == (RING - 1) * STAGE ? 0 : cur + STAGE);
+    const int nxt = opaque(cur == ring + (RING - 1) * STAGE ? ring : cur + STAGE);
     auto w = [&](int j) -> u4 (&)[2] { return j < HALF ? early[j] : late[j - HALF]; };
     u4 half[FAST ? 1 : NI][4];
     if constexpr (!FAST) {
@@ -838,11 +925,28 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args a, int til
     stage(it + 1, other, late, first, ws_next, ws);
   }
   if (it < stages) stage(it, first, late, other, ws, ws_next);
+  }
 #pragma unroll
   for (int t = MI * NI - LAG; t < MI * NI; ++t) join(t - MI * NI);
   wait_loads<0>();   // nothing is on its way to LDS any more
   barrier();
-  uint8_t* const strip = smem + wave * (16 * (16 * NI + 4) * 4);
+  if constexpr (KG > 1) {
+    static_assert((KG - 1) * TM * TN * 4 <= KG * RING * STAGE, "the other groups' sums");
+    f4* const sums = reinterpret_cast<f4*>(smem) + wave * (MI * NI * 64) + lane;
+    if (kg > 0) {
+#pragma unroll
+      for (int t = 0; t < MI * NI; ++t) sums[(kg - 1) * (TM * TN / 4) + t * 64] = acc[t / NI][t % NI];
+    }
+    wait_lds();
+    barrier();
+    if (kg > 0) return;
+#pragma unroll
+    for (int k = 0; k < KG - 1; ++k)
+#pragma unroll
+      for (int t = 0; t < MI * NI; ++t) acc[t / NI][t % NI] += sums[k * (TM * TN / 4) + t * 64];
+  }
+  // (of several groups the first one's waves alone are left: a wave reads its own sums before its strip takes their place)
+  uint8_t* const strip = smem + wave * (KG > 1 ? MI * NI * 1024 : 16 * (16 * NI + 4) * 4);
   const int m = m0 + wm * MI * 16, n = n0 + wn * NI * (MODE == PRODUCT ? 16 : 8);
   if constexpr (FAST) {
     f8_store_as<MODE, BF16, MI, NI>(a, strip, m, n, acc);
@@ -856,46 +960,71 @@ __global__ __launch_bounds__(WM * WN * 64) void f8_tile_kernel(F8Args a, int til
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+// Which kernel takes a product.  tile 0: f8_rows_kernel with nw waves a workgroup; 1..5: f8_tile_kernel on F8_TILES.
+// QF8_TILE=0..5 in the environment forces one (tests, tuning).  fits: whether a grid holds it.
 struct F8Plan { int tile, nw; int64_t workgroups; bool fits; };
 
 // What the tiles multiply with: 16-bit x, 8-bit x on converted codes, 8-bit x as it is.
 enum { KIND_16 = 0, KIND_EXACT = 1, KIND_FAST = 2 };
-struct F8Tile { int rows, cols, threads; };
-constexpr F8Tile F8_TILES[3][3] = {{{64, 64, 256}, {128, 128, 512}, {128, 256, 512}},
-                                   {{64, 64, 256}, {128, 128, 512}, {128, 256, 512}},
-                                   {{64, 64, 256}, {128, 128, 256}, {256, 256, 512}}};
 
-int64_t f8_grid(int M, int64_t w_rows, const F8Tile& t) {
-  return (((int64_t)M + t.rows - 1) / t.rows * ((w_rows + t.cols - 1) / t.cols) + 7) / 8 * 8;
+// The rule is a model of the time in nanoseconds, fitted to what the kernels took in replayed graphs (48 random
+// shapes of 1..4096 rows, plain and gated, of each kind: the tile it picks is 0.8 % behind the best on average).  A
+// tile's stage of 128 k takes `alone` when its CU runs one tile and `shared` for each of the CU's tiles when the
+// chip is full; `start` is a tile's first loads and stores, of which the share `more` shows again for every further
+// tile of the CU.  The rows kernel takes 1.3 to 1.9 for a block of 16 x 16 outputs and chunk of 512 k, over the whole chip.
+// For instance 8-bit x to bf16: 383 x 2048 x 4128 on 64 x 64 tiles 15.9 us, on 128 x 128 27; 4096 x
+// 8192 x 8192 on 256 x 256 265, on 128 x 128 403.  The last tile is the first with two groups of waves: 128 x 2048 x
+// 8192 with bf16 x 24.5 us, with one group 32.9; where there are several tiles for a CU they only cost.  Tiles of 64 x
+// 128 and 128 x 128 with two groups were built too and never paid.
+struct F8Tile { int rows, cols, groups, waves; double alone, shared, start, more; };   // waves: of a group
+constexpr F8Tile F8_TILES[3][5] = {
+    {{64, 64, 1, 4, 462, 379, 3850, 0.34}, {64, 128, 1, 4, 847, 584, 3470, 0.56}, {128, 128, 1, 8, 850, 853, 5150, 1.21},
+     {128, 256, 1, 8, 1455, 1455, 5840, 1.91}, {64, 64, 2, 4, 499, 651, 4550, 0.73}},
+    {{64, 64, 1, 4, 470, 373, 3830, 0.36}, {64, 128, 1, 4, 679, 537, 4110, 0.56}, {128, 128, 1, 8, 952, 1006, 5140, 1.41},
+     {128, 256, 1, 8, 1590, 1626, 6010, 2.55}, {64, 64, 2, 4, 507, 717, 4490, 0.77}},
+    {{64, 64, 1, 4, 276, 276, 3660, 0.28}, {64, 128, 1, 4, 388, 388, 3740, 0.37}, {128, 128, 1, 4, 639, 657, 4980, 1.01},
+     {256, 256, 1, 8, 1406, 1406, 7050, 0.27}, {64, 64, 2, 4, 327, 486, 4110, 0.72}}};
+
+int64_t f8_pieces(int64_t M, int64_t w_rows, const F8Tile& t) {
+  return (M + t.rows - 1) / t.rows * ((w_rows + t.cols - 1) / t.cols);
 }
+int64_t f8_grid(int64_t M, int64_t w_rows, const F8Tile& t) { return (f8_pieces(M, w_rows, t) + 7) / 8 * 8; }
 
 // N: columns of y, or features of a gated form.  pitch: bytes from one row of x to the next.
 F8Plan plan_f8(int mode, int M, int N, int K, int64_t pitch, int kind) {
   F8Plan p = {0, 1, 0, true};
   if (M == 0 || N == 0) return p;
-  const int64_t chunks = ((int64_t)K + 511) / 512, w_rows = mode == PRODUCT ? N : 2 * (int64_t)N;
+  const int64_t chunks = ((int64_t)K + 511) / 512, stages = ((int64_t)K + 127) / 128;
+  const int64_t w_rows = mode == PRODUCT ? N : 2 * (int64_t)N, row_tiles = ((int64_t)M + 15) / 16;
   // The tiles' buffers hold 256 rows of codes, or 128 of 16-bit x, in less than 2^31 bytes.  A larger pitch is the rows kernel's.
   if (K > 0 && pitch <= (1 << 22)) {
-    if (M > 16) p.tile = 1;
-    if (M > 64 && (int64_t)M * w_rows >= 128 * 128 * 256) p.tile = 2;
-    if (M > 128 && (int64_t)M * w_rows >= 256 * 256 * 200) p.tile = 3;
+    double best = 3200 + (1.25 + 0.04 * std::min(M, 16)) * (double)(row_tiles * ((w_rows + 15) / 16) * chunks) + 120 * (double)chunks;
+    if (row_tiles > 65535) best = 1e300;   // the rows kernel's grid
+    for (int i = 0; i < 5; ++i) {
+      const F8Tile& t = F8_TILES[kind][i];
+      const double turns = (double)((f8_pieces(M, w_rows, t) + 255) / 256);
+      const double cost = (double)((stages + t.groups - 1) / t.groups) * std::max(t.alone, t.shared * turns) +
+                          t.start * (1 + t.more * (turns - 1));
+      if (cost < best) best = cost, p.tile = i + 1;
+    }
     const int forced = env_int("QF8_TILE", -1);
-    if (forced >= 0 && forced <= 3) p.tile = forced;
+    if (forced >= 0 && forced <= 5) p.tile = forced;
   }
   if (p.tile) {
     const F8Tile& t = F8_TILES[kind][p.tile - 1];
-    p.workgroups = ((int64_t)M + t.rows - 1) / t.rows * ((w_rows + t.cols - 1) / t.cols);
-    p.fits = f8_grid(M, w_rows, t) * t.threads <= (int64_t)UINT32_MAX;
+    p.nw = 0;
+    p.workgroups = f8_pieces(M, w_rows, t);
+    p.fits = f8_grid(M, w_rows, t) * t.waves * t.groups * 64 <= (int64_t)UINT32_MAX;
     return p;
   }
   // a wave for every chunk, as far as LDS holds x and the sums for them
   p.nw = chunks <= 1 ? 1 : chunks <= 2 ? 2 : chunks <= 4 ? 4 : chunks <= 8 ? 8 : 16;
   const int rows = std::min(M, 16), nt = mode == PRODUCT ? 1 : 2;
   while (p.nw * ((kind != KIND_16 ? (rows + 1) / 2 : rows) + 2 * nt) > 160) p.nw /= 2;
-  p.workgroups = ((int64_t)M + 15) / 16 * (((int64_t)N + 15) / 16);
+  p.workgroups = row_tiles * (((int64_t)N + 15) / 16);
   // 16 waves have 128 registers each: enough for one chunk a wave and one block a workgroup, not for the next ones' weights
   if (p.nw == 16 && (chunks > 16 || p.workgroups > 256 * 2)) p.nw = 8;
-  p.fits = ((int64_t)M + 15) / 16 <= 65535;
+  p.fits = row_tiles <= 65535;
   return p;
 }
 
@@ -916,24 +1045,25 @@ template <int XT, int MODE, int NW, bool ROWS> void launch_rows(const F8Args& a,
   hipLaunchKernelGGL((f8_rows_kernel<XT, MODE, NW, false, ROWS>), grid, dim3(NW * 64), lds, s, a);
 }
 
-template <int XT, bool FAST, int MODE, bool ROWS, int MI, int NI, int WM, int WN, int RING>
+template <int XT, bool FAST, int MODE, bool ROWS, int TILE, int MI, int NI, int WM, int WN, int RING>
 void launch_tiles(const F8Args& a, hipStream_t s) {
-  constexpr F8Tile t = {16 * MI * WM, 16 * NI * WN, WM * WN * 64};
-  static_assert(t.rows == F8_TILES[FAST ? KIND_FAST : XT == F8 ? KIND_EXACT : KIND_16][0].rows ||
-                t.rows >= F8_TILES[FAST ? KIND_FAST : XT == F8 ? KIND_EXACT : KIND_16][1].rows, "as planned");
+  constexpr F8Tile t = F8_TILES[FAST ? KIND_FAST : XT == F8 ? KIND_EXACT : KIND_16][TILE - 1];
+  static_assert(t.rows == 16 * MI * WM && t.cols == 16 * NI * WN && t.waves == WM * WN, "as planned");
   const dim3 grid((unsigned)f8_grid(a.M, a.w_rows, t));
-  hipLaunchKernelGGL((f8_tile_kernel<XT, FAST, MODE, ROWS, MI, NI, WM, WN, RING>), grid, dim3(t.threads), 0, s, a,
-                     (a.M + t.rows - 1) / t.rows, (int)(((int64_t)a.w_rows + t.cols - 1) / t.cols));
+  hipLaunchKernelGGL((f8_tile_kernel<XT, FAST, MODE, ROWS, MI, NI, WM, WN, RING, t.groups>), grid, dim3(t.waves * t.groups * 64),
+                     0, s, a, (a.M + t.rows - 1) / t.rows, (int)(((int64_t)a.w_rows + t.cols - 1) / t.cols));
 }
 
 template <int XT, bool FAST, int MODE, bool ROWS> void launch_f8(const F8Args& a, const F8Plan& p, hipStream_t s) {
-  if (p.tile == 1) return launch_tiles<XT, FAST, MODE, ROWS, 2, 2, 2, 2, XT == F8 ? 4 : 3>(a, s);
+  if (p.tile == 1) return launch_tiles<XT, FAST, MODE, ROWS, 1, 2, 2, 2, 2, XT == F8 ? 4 : 3>(a, s);
+  if (p.tile == 2) return launch_tiles<XT, FAST, MODE, ROWS, 2, 2, 4, 2, 2, XT == F8 ? 3 : 2>(a, s);
+  if (p.tile == 5) return launch_tiles<XT, FAST, MODE, ROWS, 5, 2, 2, 2, 2, XT == F8 ? 4 : 3>(a, s);
   if constexpr (FAST) {
-    if (p.tile == 2) return launch_tiles<XT, FAST, MODE, ROWS, 4, 4, 2, 2, 4>(a, s);
-    if (p.tile == 3) return launch_tiles<XT, FAST, MODE, ROWS, 8, 4, 2, 4, 2>(a, s);
+    if (p.tile == 3) return launch_tiles<XT, FAST, MODE, ROWS, 3, 4, 4, 2, 2, 4>(a, s);
+    if (p.tile == 4) return launch_tiles<XT, FAST, MODE, ROWS, 4, 8, 4, 2, 4, 2>(a, s);
   } else {
-    if (p.tile == 2) return launch_tiles<XT, FAST, MODE, ROWS, 4, 2, 2, 4, XT == F8 ? 4 : 3>(a, s);
-    if (p.tile == 3) return launch_tiles<XT, FAST, MODE, ROWS, 4, 4, 2, 4, XT == F8 ? 3 : 2>(a, s);
+    if (p.tile == 3) return launch_tiles<XT, FAST, MODE, ROWS, 3, 4, 2, 2, 4, XT == F8 ? 4 : 3>(a, s);
+    if (p.tile == 4) return launch_tiles<XT, FAST, MODE, ROWS, 4, 4, 4, 2, 4, XT == F8 ? 3 : 2>(a, s);
   }
   if constexpr (!FAST) {
     if (p.nw == 1) return launch_rows<XT, MODE, 1, ROWS>(a, s);
@@ -944,8 +1074,14 @@ template <int XT, bool FAST, int MODE, bool ROWS> void launch_f8(const F8Args& a
   }
 }
 
+// bf16 results keep 8 bits: what 8-bit matrix instructions cut (see mfma_f8) is a tenth of their rounding.  fp16 and
+// fp32 results, and products of blocks of 1 (weights' gradients), take converted codes, whose sums are as exact as fp32.
+int f8_kind(int x_type, int y_type, int w_block) {
+  return x_type != F8 ? KIND_16 : y_type == BF16 && w_block == 128 ? KIND_FAST : KIND_EXACT;
+}
+
 template <int MODE> int run_f8(const F8Args& a, int x_type, int w_block, void* stream) {
-  const int kind = x_type != F8 ? KIND_16 : a.y_type == BF16 && w_block == 128 ? KIND_FAST : KIND_EXACT;
+  const int kind = f8_kind(x_type, a.y_type, w_block);
   const F8Plan p = plan_f8(MODE, a.M, MODE == PRODUCT ? a.N : a.F, a.K, a.ldx_bytes, kind);
   if (!p.fits) return QG_E_UNSUPPORTED;
   int st = device_present();
@@ -994,7 +1130,7 @@ int setup_f8(const void* x, int ldx, int x_type, const float* xs, const uint8_t*
   return QG_OK;
 }
 
-int check_act(int act, int F) { return (act == QG_ACT_SILU || act == QG_ACT_GELU_TANH) && F >= 0 && F % 16 == 0 && F <= INT_MAX / 2 ? QG_OK : QG_E_ARG; }
+int check_act(int act, int F) { return (act == QG_ACT_SILU || act == QG_ACT_GELU_TANH) && F >= 0 && F % 16 == 0 && F <= INT_MAX / 2 - 512 ? QG_OK : QG_E_ARG; }
 
 template <int T>
 void launch_quantize(const void* v, int ldx, int M, int K, int block, bool turn, uint8_t* codes, float* scales, hipStream_t s) {
@@ -1018,6 +1154,18 @@ void launch_quantize(const void* v, int ldx, int M, int K, int block, bool turn,
 }  // namespace qg
 
 using namespace qg;
+
+extern "C" int qf8_plan(int gated, int M, int N, int K, int x_type, int y_type, int w_block, int out[3]) {
+  if ((gated != 0 && gated != 1) || M < 0 || N < 0 || K < 0 || K % 16 || (x_type != F16 && x_type != BF16 && x_type != F8) ||
+      !float_type(y_type) || (w_block != 1 && w_block != 128) || (w_block == 1 && x_type != F8) || (gated && N % 16) || !out)
+    return QG_E_ARG;
+  if (M > INT_MAX - 512 || N > (gated ? INT_MAX / 2 : INT_MAX) - 512 || K > INT_MAX - 512) return QG_E_UNSUPPORTED;
+  const F8Plan p = plan_f8(gated ? GATED : PRODUCT, M, N, K, (int64_t)K * (x_type == F8 ? 1 : 2), f8_kind(x_type, y_type, w_block));
+  out[0] = p.tile;
+  out[1] = p.nw;
+  out[2] = (int)std::min<int64_t>(p.workgroups, INT_MAX);
+  return QG_OK;
+}
 
 extern "C" int qf8_quantize(const void* x, int ldx, int x_type, int M, int K, int block, int transpose, uint8_t* codes,
                             float* scales, void* stream) {

@@ -281,3 +281,63 @@ def test_binding_refuses_cpu_tensors():
                  lambda: qgm.F8Linear.from_weight(x), lambda: qgm.F8Gated.from_weight(x)):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+# --------------------------------------------------------------- the plans
+
+def test_plans(monkeypatch):
+    plan = qgm.f8_plan
+    # few rows: a wave for each chunk of 512 k, as far as LDS holds 16 rows of x for them
+    assert plan(1, 6144, 2048, F16, F16) == dict(tile=0, waves=4, pieces=384)
+    assert plan(8, 2048, 8192, BF16) == dict(tile=0, waves=16, pieces=128)
+    assert plan(1, 8192, 2048, F16, F16, gated=True) == dict(tile=0, waves=4, pieces=512)
+    assert plan(16, 2048, 8192, BF16)["waves"] == 8 and plan(1, 64, 96, BF16)["waves"] == 1
+    assert plan(1, 64, 0, BF16)["tile"] == 0
+    # larger tiles as the rows grow
+    tiles = [plan(m, 8192, 8192, F8)["tile"] for m in (1, 100, 1000, 4096)]
+    assert tiles[0] == 0 and tiles[1] in (1, 2, 5) and tiles[-1] == 4
+    assert plan(4096, 8192, 8192, F8) == dict(tile=4, waves=0, pieces=512)
+    assert plan(4096, 8192, 8192, F8, F32)["pieces"] == 1024 == plan(4096, 8192, 8192, F8, w_block=1)["pieces"]
+    assert plan(128, 2048, 8192, BF16)["tile"] == 5      # few tiles of a long K: two groups of waves
+    # the rows kernel's grid has 65535 blocks of 16 rows; rows of more than 4 MiB are its alone
+    assert plan(1 << 21, 16, 16, BF16)["tile"] > 0
+    assert plan(4096, 4096, 1 << 23, F8)["tile"] == 0 and plan(4096, 4096, 1 << 22, F8)["tile"] > 0
+    for v in range(6):
+        monkeypatch.setenv("QF8_TILE", str(v))
+        assert plan(100, 300, 512, F16)["tile"] == v and plan(100, 304, 512, F8, gated=True)["tile"] == v
+    out = (qgm.ctypes.c_int * 3)()
+    for bad in ((2, 1, 1, 16, 0, 0, 128), (0, -1, 1, 16, 0, 0, 128), (0, 1, -1, 16, 0, 0, 128), (0, 1, 1, 24, 0, 0, 128),
+                (0, 1, 1, 16, 2, 0, 128), (0, 1, 1, 16, 0, 4, 128), (0, 1, 1, 16, 0, 0, 1), (0, 1, 1, 16, 4, 0, 64),
+                (1, 1, 8, 16, 0, 0, 128)):
+        assert lib.qf8_plan(*bad, out) == E_ARG
+    assert lib.qf8_plan(0, 1, 1, 16, 0, 0, 128, None) == E_ARG
+    top = (1 << 31) - 1
+    for bad in ((0, top, 16, 16, 0, 0, 128), (0, 16, top, 16, 0, 0, 128), (1, 16, 1 << 30, 16, 0, 0, 128)):
+        assert lib.qf8_plan(*bad, out) == E_UNSUP
+
+
+@pytest.mark.parametrize("M,N", [(0, 16), (16, 0), (0, 0)])
+def test_plan_of_nothing(M, N):
+    for K in (0, 64, 8192):
+        for x_type in (F16, BF16, F8):
+            assert qgm.f8_plan(M, N, K, x_type) == dict(tile=0, waves=1, pieces=0)
+
+
+@pytest.mark.parametrize("tile,call", [
+    (0, lambda: gemm(M=65535 * 16 + 1)), (1, lambda: gemm(M=1 << 18, N=1 << 18)), (5, lambda: gemm(M=1 << 18, N=1 << 17)),
+    (4, lambda: gemm(xt=F8, xs=A, yt=BF16, M=1 << 20, N=1 << 19)), (0, lambda: gated(M=65535 * 16 + 1)),
+    (None, lambda: gemm(M=(1 << 20), K=0)), (None, lambda: gemm(M=1 << 20, K=1 << 23, xt=F8, xs=A))])
+def test_more_than_a_grid_holds(monkeypatch, tile, call):
+    if tile is not None:
+        monkeypatch.setenv("QF8_TILE", str(tile))
+    assert call() == E_UNSUP
+
+
+@pytest.mark.skipif(gpu_present(), reason="checks the no-device status; a GPU is present")
+@pytest.mark.parametrize("tile,call", [
+    (0, lambda: gemm(M=65535 * 16)), (1, lambda: gemm(M=(1 << 18) - 64, N=1 << 18)),
+    (4, lambda: gemm(xt=F8, xs=A, yt=BF16, M=(1 << 20) - 256, N=1 << 19)), (None, lambda: gemm(M=1 << 22))])
+def test_what_a_grid_holds_comes_to_the_device(monkeypatch, tile, call):
+    if tile is not None:
+        monkeypatch.setenv("QF8_TILE", str(tile))
+    assert call() == E_DEVICE

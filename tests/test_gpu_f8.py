@@ -370,7 +370,7 @@ EVERY = [(1, 129, 512), (70, 257, 528), (17, 64, 992), (130, 300, 1024), (260, 7
          (5, 17, 16), (129, 513, 480), (33, 100, 2512), (300, 530, 144), (600, 1100, 272)]
 
 
-@pytest.mark.parametrize("tile", range(4))
+@pytest.mark.parametrize("tile", range(6))
 @pytest.mark.parametrize("kind", KINDS + ["rows"])
 @pytest.mark.parametrize("M,N,K", EVERY)
 def test_gemm_every_kernel(monkeypatch, tile, kind, M, N, K):
@@ -401,7 +401,7 @@ def test_gemm_every_kernel(monkeypatch, tile, kind, M, N, K):
         inside(y[:, torch.from_numpy(keep).to(DEV)], ref[:, keep], tol[:, keep])
 
 
-@pytest.mark.parametrize("tile", range(4))
+@pytest.mark.parametrize("tile", range(6))
 @pytest.mark.parametrize("kind", KINDS)
 def test_gemm_past_k_is_not_read_into_sums(monkeypatch, tile, kind):
     # rows whose neighbours in memory are NaN: x with a wide pitch, the last row of W before other codes
@@ -426,7 +426,7 @@ def test_gemm_past_k_is_not_read_into_sums(monkeypatch, tile, kind):
                sums(K, mag) + cut(x, xs, wc, ws, yt))
 
 
-@pytest.mark.parametrize("tile", range(4))
+@pytest.mark.parametrize("tile", range(6))
 @pytest.mark.parametrize("kind", ["bf16", "f8"])
 def test_gemm_far_rows(monkeypatch, tile, kind):
     # rows of x, of W and of y that lie more than 4 GiB into their arrays
@@ -485,7 +485,7 @@ def gate_tolerances(x, w, act, K, left=0.0):
     return h, th, (g, u, a, da, eg, eu, ea, t)
 
 
-@pytest.mark.parametrize("tile", [None, 0, 1, 2, 3])
+@pytest.mark.parametrize("tile", [None, 0, 1, 2, 3, 4, 5])
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("M,F,K", GATED)
@@ -504,7 +504,7 @@ def test_gated(monkeypatch, tile, kind, act, M, F, K):
         assert bool((out[M] == 9).all()) and bool((out[:, F:] == 9).all())
 
 
-@pytest.mark.parametrize("tile", [None, 0, 1, 2, 3])
+@pytest.mark.parametrize("tile", [None, 0, 1, 2, 3, 4, 5])
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("M,F,K", GATED)
