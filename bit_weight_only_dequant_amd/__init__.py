@@ -767,11 +767,12 @@ def f8_quantize(x, block=1, transpose=False, codes=None, scales=None, stream=Non
     if block not in (1, 128):
         raise ValueError(f"block must be 1 or 128; got {block!r}")
     R, C = (K, (M + 15) // 16 * 16) if transpose else (M, K)
+    given = codes is not None or scales is not None
     if codes is None:
         codes = x.new_empty((R, C), dtype=_CODE)
     if scales is None:
         scales = x.new_empty((R if block == 1 else _f8_blocks(R), _f8_blocks(C)), dtype=_F32)
-    if _f8_matrix(codes, scales, "codes and scales", dev, block)[:2] != (R, C):
+    if given and _f8_matrix(codes, scales, "codes and scales", dev, block)[:2] != (R, C):
         raise ValueError(f"codes must be [{R}, {C}]")
     st = _lib.qf8_quantize(x.data_ptr(), ldx, xt, M, K, block, 1 if transpose else 0, codes.data_ptr(),
                            scales.data_ptr(), _mx_stream(dev))

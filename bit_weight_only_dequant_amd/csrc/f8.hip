@@ -273,34 +273,68 @@ __device__ __forceinline__ Gate gate(float g, int act) {
   return {g * s, s + h * (s * s1) * dt};
 }
 
-// C consecutive features of row m from feature f on: their two projections to
-// what is stored.
+// C consecutive outputs at y, `have` of them (C or more: all), rounded once.
+template <typename E, int C> __device__ __forceinline__ void put_rounded(E* y, int have, const float (&v)[C]) {
+  E q[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) q[i] = (E)v[i];
+  if (have >= C) put(y, q);
+  else for (int i = 0; i < C; ++i) if (i < have) y[i] = q[i];
+}
+
+// What an output needs beside its sums, C columns (of a gated form: features) from n on of row m: the residual, or
+// dh.  Zeros without one.
 template <int MODE, int YT, int C>
-__device__ __forceinline__ void store_gated_as(const F8Args& a, int m, int f, float (&g)[C], float (&u)[C]) {
+__device__ __forceinline__ void load_beside(const F8Args& a, int m, int n, typename Elem<YT>::type (&e)[C]) {
   typedef typename Elem<YT>::type E;
-  if constexpr (MODE == GATED) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) g[i] = gate(g[i], a.act).value * u[i];
-    store_cols_as<YT, C>(a, m, f, g, 1.f);
-  } else {
-    E d[C];
-    get(reinterpret_cast<const E*>(a.dh) + (int64_t)m * a.ldd + f, d);
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const Gate v = gate(g[i], a.act);
-      const float dh = to_f32(d[i]);
-      g[i] = dh * u[i] * v.slope;
-      u[i] = dh * v.value;
-    }
-    store_cols_as<YT, C>(a, m, f, g, 1.f);
-    store_cols_as<YT, C>(a, m, a.F + f, u, 1.f);
+  for (int i = 0; i < C; ++i) e[i] = (E)0.f;
+  if (m >= a.M) return;
+  if constexpr (MODE == GRAD) {
+    if (n < a.F) get(reinterpret_cast<const E*>(a.dh) + (int64_t)m * a.ldd + n, e);
+  } else if constexpr (MODE == PRODUCT) {
+    if (!a.resid || n >= a.N) return;
+    const E* p = reinterpret_cast<const E*>(a.resid) + (int64_t)m * a.ldr + n;
+    if (n + C <= a.N) get(p, e);
+    else for (int i = 0; i < C; ++i) if (i < a.N - n) e[i] = p[i];
   }
 }
-template <int MODE, int C>
-__device__ __forceinline__ void store_gated(const F8Args& a, int m, int f, float (&g)[C], float (&u)[C]) {
-  if (a.y_type == F32) store_gated_as<MODE, F32, C>(a, m, f, g, u);
-  else if (a.y_type == F16) store_gated_as<MODE, F16, C>(a, m, f, g, u);
-  else store_gated_as<MODE, BF16, C>(a, m, f, g, u);
+
+// Stores them: v the sums (of a gated form the gate's, u the other projection's), e what load_beside() gave.
+template <int MODE, int YT, int C>
+__device__ __forceinline__ void store_outputs(const F8Args& a, int m, int n, float (&v)[C], float (&u)[C],
+                                              const typename Elem<YT>::type (&e)[C]) {
+  typedef typename Elem<YT>::type E;
+  E* const y = reinterpret_cast<E*>(a.y) + (int64_t)m * a.ldy + n;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    if constexpr (MODE == PRODUCT) {
+      if (a.resid) v[i] += to_f32(e[i]);
+    } else {
+      const Gate g = gate(v[i], a.act);
+      if constexpr (MODE == GATED) {
+        v[i] = g.value * u[i];
+      } else {
+        const float dh = to_f32(e[i]);
+        v[i] = dh * u[i] * g.slope;
+        u[i] = dh * g.value;
+      }
+    }
+  }
+  put_rounded(y, MODE == PRODUCT ? a.N - n : C, v);
+  if constexpr (MODE == GRAD) put_rounded(y + a.F, C, u);
+}
+
+template <int MODE, int YT>
+__device__ __forceinline__ void store_four_as(const F8Args& a, int m, int n, float (&v)[4], float (&u)[4]) {
+  typename Elem<YT>::type e[4];
+  load_beside<MODE, YT, 4>(a, m, n, e);
+  store_outputs<MODE, YT, 4>(a, m, n, v, u, e);
+}
+template <int MODE> __device__ __forceinline__ void store_four(const F8Args& a, int m, int n, float (&v)[4], float (&u)[4]) {
+  if (a.y_type == F32) store_four_as<MODE, F32>(a, m, n, v, u);
+  else if (a.y_type == F16) store_four_as<MODE, F16>(a, m, n, v, u);
+  else store_four_as<MODE, BF16>(a, m, n, v, u);
 }
 
 // 8 codes -> 8 exact 16-bit values (E4M3 lies within fp16's and bf16's numbers)
@@ -499,12 +533,8 @@ __global__ __launch_bounds__(NW * 64) void f8_rows_kernel(F8Args a) {
       const int n = nb * 16 + 4 * g;
       if (r < rows && n < (MODE == PRODUCT ? a.N : a.F)) {
         float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-        if constexpr (MODE == PRODUCT) {
-          store_cols<4>(a, m0 + r, n, o, 1.f);
-        } else {
-          float u[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
-          store_gated<MODE, 4>(a, m0 + r, n, o, u);
-        }
+        float u[4] = {v[NT - 1].x, v[NT - 1].y, v[NT - 1].z, v[NT - 1].w};
+        store_four<MODE>(a, m0 + r, n, o, u);
       }
     }
     buf ^= 1;
@@ -561,13 +591,23 @@ __device__ __forceinline__ bool f8_tile(int tiles_m, int tiles_n, int& tm, int& 
 // passes through LDS (the wave's own `strip`, rows padded by 16 bytes), so that
 // a lane stores 8 consecutive outputs.  Gated forms have gate and other
 // projection in turn, 16 features each.
+// The residual's (or dh's) pieces of a strip are sent for two strips ahead.
 template <int MODE, int YT, int MI, int NI>
 __device__ __forceinline__ void f8_store_as(const F8Args& a, uint8_t* strip, int m0, int n0, const f4 (&acc)[MI][NI]) {
+  typedef typename Elem<YT>::type E;
   constexpr int PITCH = 16 * NI + 4, PARTS = MODE == PRODUCT ? 1 : 2;
   constexpr int LANES = 2 * NI / PARTS, ROWS = 64 / LANES;   // lanes a row, rows at a time
-  const int lane = threadIdx.x & 63, c = lane % LANES;
+  constexpr int PASSES = (16 + ROWS - 1) / ROWS;
+  const int lane = threadIdx.x & 63, c = lane % LANES, n = n0 + c * 8;
   float* s = reinterpret_cast<float*>(strip);
   const float* from = s + (MODE == PRODUCT ? c * 8 : (c >> 1) * 32 + (c & 1) * 8);
+  E beside[2][PASSES][8];
+  auto load = [&](int i) {
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) load_beside<MODE, YT, 8>(a, m0 + i * 16 + p * ROWS + lane / LANES, n, beside[i & 1][p]);
+  };
+  load(0);
+  load(1);
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
 #pragma unroll
@@ -575,22 +615,17 @@ __device__ __forceinline__ void f8_store_as(const F8Args& a, uint8_t* strip, int
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    const int n = n0 + c * 8;
 #pragma unroll
-    for (int p = 0; p < (16 + ROWS - 1) / ROWS; ++p) {
+    for (int p = 0; p < PASSES; ++p) {
       const int r = p * ROWS + lane / LANES, m = m0 + i * 16 + r;
       if (r < 16 && m < a.M && n < (MODE == PRODUCT ? a.N : a.F)) {
-        float v[8];
+        float v[8], u[8];
         __builtin_memcpy(v, from + r * PITCH, sizeof(v));
-        if constexpr (MODE == PRODUCT) {
-          store_cols_as<YT, 8>(a, m, n, v, 1.f);
-        } else {
-          float u[8];
-          __builtin_memcpy(u, from + r * PITCH + 16, sizeof(u));
-          store_gated_as<MODE, YT, 8>(a, m, n, v, u);
-        }
+        __builtin_memcpy(u, from + r * PITCH + (MODE == PRODUCT ? 0 : 16), sizeof(u));
+        store_outputs<MODE, YT, 8>(a, m, n, v, u, beside[i & 1][p]);
       }
     }
+    if (i + 2 < MI) load(i + 2);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
