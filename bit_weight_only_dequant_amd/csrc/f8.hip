@@ -667,6 +667,7 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
   constexpr int SROWS = (C8 ? TM : 0) + (ROWS ? TN : 0), SOFF = C8 ? TM : 0;
   static_assert(SROWS % 64 == 0 && SOFF % 64 == 0, "a load brings the scales of 64 rows, of x or of W");
   constexpr int SL = SROWS / 64 > 0 ? SROWS / 64 : 1, QS = (SROWS / 64 + NW - 1) / NW, QALL = QD + QS;   // such loads, and a wave's
+  constexpr bool WHOLE = MI * NI <= (FAST ? 16 : 8);   // a stage's fragments are read during the one before (below)
   constexpr int PIECES = TM * XB + TN * 128, STAGE = PIECES + SROWS * 4;
   static_assert(NW * 16 * (16 * NI + 4) * 4 <= RING * STAGE && (KG == 1 || 16 * (16 * NI + 4) <= MI * NI * 256),
                 "the strips of f8_store_as: a wave's lies within its own part of the sums");
@@ -756,7 +757,6 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
   // registers hold two stages' of them.  Else x is read one row of blocks ahead, and the last row goes through its
   // blocks from HALF on and around: the fragments of the others, which it needs last, have a second place (`other`),
   // the later ones are read again as soon as it has used them.
-  constexpr bool WHOLE = MI * NI <= (FAST ? 16 : 8);
   constexpr int HALF = NI / 2;
   auto block = [](int i, int s) { return !WHOLE && i == MI - 1 ? (s + HALF) % NI : s; };   // the block in turn s of row i
   u4 first[HALF][2], late[HALF][2], other[HALF][2];
@@ -811,11 +811,16 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
     }
   };
 
+  // Of a stage's loads the first EARLY are sent for in the last row of blocks, the others along the next stage's first
+  // rows (where all is read ahead: all along the stage).  All in the last row made its waves wait to send: 4096 x 8192 x
+  // 8192 took 306 us there instead of 291, and with 16-bit x 4096 x 2048 x 16384 253 instead of 245.
+  constexpr int EARLY = WHOLE ? QALL : C8 ? 4 : 6;
+  static_assert(WHOLE || (EARLY <= QALL && (QALL - EARLY - 1) * 2 + 1 < (MI - 1) * NI), "the others are sent for in time");
 #pragma unroll
   for (int it = 0; it < RING; ++it)
 #pragma unroll
-    for (int q = 0; q < QALL; ++q) issue(it, smem + kg * (RING * STAGE) + it * STAGE, q);
-  wait_loads<(RING - 1) * QALL>();
+    for (int q = 0; q < (it < RING - 1 ? QALL : EARLY); ++q) issue(it, smem + kg * (RING * STAGE) + it * STAGE, q);
+  wait_loads<(RING - 2) * QALL + EARLY>();
   barrier();
   const int ring = kg * (RING * STAGE);
   int cur = opaque(ring);   // the place of the stage at hand
@@ -899,6 +904,7 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
 #pragma unroll
   for (int j = 0; j < NI; ++j) read_w(cur, j, j < HALF ? first[j] : late[j - HALF]);
   read_ws(cur, 0, ws);
+  int before = ring + (RING - 1) * STAGE;   // and of the one before
   // early: the fragments of the first HALF blocks, late: those of the others; next: where the next stage's first ones go
   auto stage = [&](int it, u4 (&early)[HALF][2], u4 (&late)[HALF][2], u4 (&next)[HALF][2], F (&s)[NI], F (&s_next)[NI]) {
     const int nxt = opaque(cur == ring + (RING - 1) * STAGE ? ring : cur + STAGE);
@@ -942,15 +948,21 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
             part[p] = mfma_16<XT>(half[j][q], xh[q], q ? part[p] : f4{0.f, 0.f, 0.f, 0.f});
           }
           if (q == 0) f[p] = sx[i & 1] * s[j];
+          if (i < MI - 1 && q == 0) {
+#pragma unroll
+            for (int l = EARLY; l < QALL; ++l)
+              if ((l - EARLY) * 2 + 1 == t) issue(it - 1 + RING, smem + before, l);
+          }
           if (i == MI - 1 && q == Q - 1) {   // the loads spread over the row
 #pragma unroll
             for (int l = 0; l < QALL; ++l)
-              if (l * NI / QALL == n) issue(it + RING, smem + cur, l);
+              if (l < EARLY && l * NI / EARLY == n) issue(it + RING, smem + cur, l);
             if (j >= HALF) read_w(nxt, j, late[j - HALF]);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
     }
+    before = cur;
     cur = nxt;
   };
   int it = 0;
