@@ -717,25 +717,26 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
     const int row = MODE == PRODUCT ? min(n0 + q * 16, a.w_rows - 1) : (q & 1) * a.F + min(n0 + (q >> 1) * 16, a.F - 1);
     wsp[j] = (Scalars)(a.ws + (int64_t)(row >> 7) * a.kb);
   }
-  // load q of stage `it` into place `to`; past K zeros
+  // Load q of stage `it` into place `to`; past K zeros.  The rows are in the lanes' offsets and the scalar one lies within
+  // a row, so that no row past the last makes it larger than the buffer.
   auto issue = [&](int it, uint8_t* to, int q) {
     it = it * KG + kg;
     const int left = a.K - it * 128;       // of K, for the pieces that lie past it
+    const int along = left > 0 ? it : 0;
     if (q < QA) {
       const int n = wave * QA + q, v = (QA % XV == 0 ? q : n) % XV;
-      const uint32_t at = xpiece[v] * (C8 ? 16 : 8) < left ? xlane + xpiece[v] * 16 : PAST;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (lptr)(to + n * 1024), 16, (int)at, (int)(n * XR * xpitch + it * XB), 0, 0);
+      const uint32_t at = xpiece[v] * (C8 ? 16 : 8) < left ? xlane + xpiece[v] * 16 + n * XR * xpitch : PAST;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (lptr)(to + n * 1024), 16, (int)at, along * XB, 0, 0);
     } else if (q < QD) {
       const int n = wave * QB + q - QA, v = (QB % 2 == 0 ? q - QA : n) % 2;
       const int half = MODE == PRODUCT ? 0 : n >> 1 & 1, row = MODE == PRODUCT ? n * 8 : (n >> 2) * 16 + (n & 1) * 8;
-      const uint32_t at = wpiece[v] * 16 < left ? wlane + wpiece[v] * 16 : PAST;
+      const uint32_t at = wpiece[v] * 16 < left ? wlane + wpiece[v] * 16 + row * wpitch : PAST;
       const Buffer wb = f8_buffer(half ? wbase + (int64_t)a.F * a.K : wbase, (int64_t)wrows * a.K);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wb, (lptr)(to + TM * XB + n * 1024), 16, (int)at,
-                                               (int)(row * wpitch + it * 128), 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wb, (lptr)(to + TM * XB + n * 1024), 16, (int)at, along * 128, 0, 0);
     } else {
       const int n = (wave * QS + q - QD) % SL;
       const uint32_t at = left > 0 ? soff[q - QD] : PAST;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(C8 && n * 64 < TM ? xsb : wsb, (lptr)(to + PIECES + n * 256), 4, (int)at, it * 4, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(C8 && n * 64 < TM ? xsb : wsb, (lptr)(to + PIECES + n * 256), 4, (int)at, along * 4, 0, 0);
     }
   };
   auto barrier = [] {
@@ -760,7 +761,9 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
   constexpr int HALF = NI / 2;
   auto block = [](int i, int s) { return !WHOLE && i == MI - 1 ? (s + HALF) % NI : s; };   // the block in turn s of row i
   u4 first[HALF][2], late[HALF][2], other[HALF][2];
-  F ws[NI], ws_next[NI];   // W's scales
+  F ws[NI], ws_next[NI];   // W's scales (the first blocks join nothing, times these)
+#pragma unroll
+  for (int j = 0; j < NI; ++j) ws[j] = ws_next[j] = F{};
   // `at`: a stage's place in smem.  It is kept from the compiler where one lies (opaque()): it would hold every
   // fragment's address in a register of its own.
   auto opaque = [](int at) {
@@ -776,6 +779,7 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
     for (int j = 0; j < NI; ++j) {
       if constexpr (ROWS) to[j] = *reinterpret_cast<const f4*>(smem + (at + PIECES + (SOFF + wn * NI * 16 + 4 * g) * 4) + j * 64);
       else to[j] = wsp[j][min(it * KG + kg, a.kb - 1)];
+      if constexpr (!ROWS && KG > 1) to[j] = it * KG + kg < a.kb ? to[j] : 0.f;   // a stage past K adds nothing, whatever the last scale
     }
   };
   u4 x[2][C8 ? 2 : 4];
@@ -795,18 +799,23 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
   // the outstanding blocks' products and factors.
   constexpr int LAG = FAST ? 3 : NI, KEPT = FAST ? 4 : NI;
   static_assert(MI * NI % KEPT == 0, "the next stage's first block takes place 0 again");
+  // LATE: W's row scales would take four registers a block with x's already in them; they are multiplied in when the
+  // block joins, from the stage's own scales `s`.
+  constexpr bool LATE = ROWS && !WHOLE;
+  typedef std::conditional_t<LATE, float, F> Factor;
   f4 part[KEPT];
-  F f[KEPT];
+  Factor f[KEPT];
 #pragma unroll
   for (int t = 0; t < KEPT; ++t) {
     part[t] = f4{0.f, 0.f, 0.f, 0.f};
-    f[t] = F{};
+    f[t] = Factor{};
   }
-  auto join = [&](int t) {   // block t (counted along the rows of blocks), t < 0: of the stage before
+  auto join = [&](int t, const F (&s)[NI]) {   // block t (counted along the rows of blocks), t < 0: of the stage before
     const int at = (t + MI * NI) % (MI * NI), p = at % KEPT, i = at / NI, j = block(i, at % NI);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if constexpr (ROWS) acc[i][j][k] = fmaf(part[p][k], f[p][k], acc[i][j][k]);
+      if constexpr (LATE) acc[i][j][k] = fmaf(part[p][k], f[p] * s[j][k], acc[i][j][k]);
+      else if constexpr (ROWS) acc[i][j][k] = fmaf(part[p][k], f[p][k], acc[i][j][k]);
       else acc[i][j][k] = fmaf(part[p][k], f[p], acc[i][j][k]);
     }
   };
@@ -867,9 +876,9 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
             const int t = i * NI + j, p = t % KEPT;
             if constexpr (FAST) {
               part[p] = mfma_f8(c.w[j][0], c.w[j][1], c.x[i][0], c.x[i][1]);
-              join(t - LAG);
+              join(t - LAG, c.s);
             } else {
-              if (q == 0) join(t - LAG);
+              if (q == 0) join(t - LAG, c.s);
               part[p] = mfma_16<XT>(half[j][q], xh[q], q ? part[p] : f4{0.f, 0.f, 0.f, 0.f});
             }
             if (q == 0) f[p] = c.sx[i] * c.s[j];
@@ -942,12 +951,15 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
           const int t = i * NI + n, p = t % KEPT, j = block(i, n);
           if constexpr (FAST) {
             part[p] = mfma_f8(w(j)[0], w(j)[1], x[i & 1][0], x[i & 1][1]);
-            join(t - LAG);
+            join(t - LAG, t < LAG ? s_next : s);
           } else {
-            if (q == 0) join(t - LAG);
+            if (q == 0) join(t - LAG, t < LAG ? s_next : s);   // (the stage before's scales are still in s_next)
             part[p] = mfma_16<XT>(half[j][q], xh[q], q ? part[p] : f4{0.f, 0.f, 0.f, 0.f});
           }
-          if (q == 0) f[p] = sx[i & 1] * s[j];
+          if (q == 0) {
+            if constexpr (LATE) f[p] = sx[i & 1];
+            else f[p] = sx[i & 1] * s[j];
+          }
           if (i < MI - 1 && q == 0) {
 #pragma unroll
             for (int l = EARLY; l < QALL; ++l)
@@ -974,7 +986,7 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
   if (it < stages) stage(it, first, late, other, ws, ws_next);
   }
 #pragma unroll
-  for (int t = MI * NI - LAG; t < MI * NI; ++t) join(t - MI * NI);
+  for (int t = MI * NI - LAG; t < MI * NI; ++t) join(t - MI * NI, stages & 1 ? ws : ws_next);
   wait_loads<0>();   // nothing is on its way to LDS any more
   barrier();
   if constexpr (KG > 1) {
@@ -1004,6 +1016,21 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
   }
 }
 
+// A product without a k, one output a lane (of the gated forms a feature): the residual, or what sums of zero give.
+template <int MODE, int YT> __global__ __launch_bounds__(EW_THREADS) void f8_no_k_kernel(F8Args a) {
+  typedef typename Elem<YT>::type E;
+  const int cols = MODE == PRODUCT ? a.N : a.F;
+  const int64_t step = (int64_t)gridDim.x * EW_THREADS, n = (int64_t)a.M * cols;
+  for (int64_t i = (int64_t)blockIdx.x * EW_THREADS + threadIdx.x; i < n; i += step) {
+    const int64_t row = i / cols, col = i - row * cols;
+    E* const y = reinterpret_cast<E*>(a.y) + row * a.ldy + col;
+    float v = 0.f;
+    if (MODE == PRODUCT && a.resid) v += to_f32(reinterpret_cast<const E*>(a.resid)[row * a.ldr + col]);
+    if (MODE == GRAD) y[a.F] = (E)(v = 0.f * to_f32(reinterpret_cast<const E*>(a.dh)[row * a.ldd + col]));
+    y[0] = (E)v;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -1025,7 +1052,7 @@ enum { KIND_16 = 0, KIND_EXACT = 1, KIND_FAST = 2 };
 // 128 and 128 x 128 with two groups were built too and never paid.
 struct F8Tile { int rows, cols, groups, waves; double alone, shared, start, more; };   // waves: of a group
 constexpr F8Tile F8_TILES[3][5] = {
-    {{64, 64, 1, 4, 475, 364, 3760, 0.39}, {64, 128, 1, 4, 832, 582, 3560, 0.54}, {128, 128, 1, 8, 848, 844, 4800, 1.31},
+    {{64, 64, 1, 4, 475, 364, 3760, 0.39}, {64, 128, 1, 4, 900, 582, 3560, 0.54}, {128, 128, 1, 8, 848, 844, 4800, 1.31},
      {128, 256, 1, 8, 1455, 1455, 5810, 1.92}, {64, 64, 2, 4, 499, 695, 4550, 0.70}},
     {{64, 64, 1, 4, 468, 382, 3800, 0.35}, {64, 128, 1, 4, 676, 480, 4110, 0.49}, {128, 128, 1, 8, 988, 988, 5200, 1.42},
      {128, 256, 1, 8, 1940, 1580, 6010, 2.68}, {64, 64, 2, 4, 507, 703, 4490, 0.77}},
@@ -1071,7 +1098,7 @@ F8Plan plan_f8(int mode, int M, int N, int K, int64_t pitch, int kind) {
   p.workgroups = row_tiles * (((int64_t)N + 15) / 16);
   // 16 waves have 128 registers each: enough for one chunk a wave and one block a workgroup, not for the next ones' weights
   if (p.nw == 16 && (chunks > 16 || p.workgroups > 256 * 2)) p.nw = 8;
-  p.fits = row_tiles <= 65535;
+  p.fits = K == 0 || row_tiles <= 65535;   // without a k an elementwise kernel takes it
   return p;
 }
 
@@ -1081,7 +1108,7 @@ template <int XT, int MODE, int NW, bool ROWS> void launch_rows(const F8Args& a,
   const size_t lds = (size_t)NW * f8_x_bytes<XT>(a.M) + 2 * NW * NT * 1024;
   // column blocks a workgroup takes: no more workgroups than keep 32 waves on every CU
   const int64_t blocks = MODE == PRODUCT ? ((int64_t)a.N + 15) / 16 : a.F / 16;
-  const int64_t slots = 256 * 32 / NW, share = a.K == 0 ? 1 : (blocks * gy + slots - 1) / slots;
+  const int64_t slots = 256 * 32 / NW, share = (blocks * gy + slots - 1) / slots;
   const dim3 grid((unsigned)((blocks + share - 1) / share), (unsigned)gy);
   if constexpr (NW <= 8) {
     if (share > 1 || a.K > 512 * NW) {
@@ -1138,6 +1165,13 @@ template <int MODE> int run_f8(const F8Args& a, int x_type, int w_block, void* s
   if (st != QG_OK) return st;
   clear_pending_error();
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (a.K == 0) {
+    const dim3 grid = ew_grid(1, (int64_t)a.M * (MODE == PRODUCT ? a.N : a.F)), block(EW_THREADS);
+    if (a.y_type == F32) hipLaunchKernelGGL((f8_no_k_kernel<MODE, F32>), grid, block, 0, s, a);
+    else if (a.y_type == F16) hipLaunchKernelGGL((f8_no_k_kernel<MODE, F16>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((f8_no_k_kernel<MODE, BF16>), grid, block, 0, s, a);
+    return launch_status();
+  }
   if constexpr (MODE == PRODUCT) {
     if (w_block == 1) {
       launch_f8<F8, false, MODE, true>(a, p, s);
@@ -1298,7 +1332,7 @@ extern "C" int qf8_gated_grad(const void* dh, int lddh, const void* x, int ldx, 
   if (st == QG_OK) st = setup_f8(x, ldx, x_type, x_scales, w, w_scales, 128, M, 2 * F, 2 * F, K, d, ldd, d_type, &a);
   if (st != QG_OK) return st;
   if (M == 0 || F == 0) return QG_OK;
-  if (!dh || lddh < F) return QG_E_ARG;
+  if (!dh || lddh < F || dh == d) return QG_E_ARG;
   if (!aligned(dh, 16)) return QG_E_ALIGN;
   a.F = F;
   a.act = act;

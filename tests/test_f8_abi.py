@@ -139,7 +139,7 @@ def gated(x=A, ldx=None, xt=F16, xs=None, w=A, ws=A, act=0, M=2, N=16, K=64, y=A
     return lib.qf8_gated(x, K if ldx is None else ldx, xt, xs, w, ws, act, M, N, K, y, N if ldy is None else ldy, yt, None)
 
 
-def grad(dh=A, ldd=None, x=A, ldx=None, xt=F16, xs=None, w=A, ws=A, act=0, M=2, N=16, K=64, y=A, ldy=None, yt=F16):
+def grad(dh=2 * A, ldd=None, x=A, ldx=None, xt=F16, xs=None, w=A, ws=A, act=0, M=2, N=16, K=64, y=A, ldy=None, yt=F16):
     return lib.qf8_gated_grad(dh, N if ldd is None else ldd, x, K if ldx is None else ldx, xt, xs, w, ws, act, M, N, K, y,
                               2 * N if ldy is None else ldy, yt, None)
 
@@ -191,7 +191,7 @@ def test_gated_refuses(kw, expect):
 
 
 @pytest.mark.parametrize("kw,expect", PRODUCT_REFUSALS + GATED_REFUSALS + [
-    (dict(dh=None), E_ARG), (dict(ldd=8), E_ARG), (dict(ldy=31), E_ARG), (dict(dh=A + 2), E_ALIGN)])
+    (dict(dh=None), E_ARG), (dict(dh=A), E_ARG), (dict(ldd=8), E_ARG), (dict(ldy=31), E_ARG), (dict(dh=A + 2), E_ALIGN)])
 def test_grad_refuses(kw, expect):
     assert grad(**kw) == expect
 
@@ -326,7 +326,7 @@ def test_plan_of_nothing(M, N):
 @pytest.mark.parametrize("tile,call", [
     (0, lambda: gemm(M=65535 * 16 + 1)), (1, lambda: gemm(M=1 << 18, N=1 << 18)), (5, lambda: gemm(M=1 << 18, N=1 << 17)),
     (4, lambda: gemm(xt=F8, xs=A, yt=BF16, M=1 << 20, N=1 << 19)), (0, lambda: gated(M=65535 * 16 + 1)),
-    (None, lambda: gemm(M=(1 << 20), K=0)), (None, lambda: gemm(M=1 << 20, K=1 << 23, xt=F8, xs=A))])
+    (None, lambda: gemm(M=1 << 20, K=1 << 23, xt=F8, xs=A))])
 def test_more_than_a_grid_holds(monkeypatch, tile, call):
     if tile is not None:
         monkeypatch.setenv("QF8_TILE", str(tile))
@@ -336,7 +336,8 @@ def test_more_than_a_grid_holds(monkeypatch, tile, call):
 @pytest.mark.skipif(gpu_present(), reason="checks the no-device status; a GPU is present")
 @pytest.mark.parametrize("tile,call", [
     (0, lambda: gemm(M=65535 * 16)), (1, lambda: gemm(M=(1 << 18) - 64, N=1 << 18)),
-    (4, lambda: gemm(xt=F8, xs=A, yt=BF16, M=(1 << 20) - 256, N=1 << 19)), (None, lambda: gemm(M=1 << 22))])
+    (4, lambda: gemm(xt=F8, xs=A, yt=BF16, M=(1 << 20) - 256, N=1 << 19)), (None, lambda: gemm(M=1 << 22)), (None, lambda: gemm(M=1 << 22, K=0)),
+    (None, lambda: gated(M=1 << 22, K=0)), (None, lambda: grad(M=1 << 22, K=0))])
 def test_what_a_grid_holds_comes_to_the_device(monkeypatch, tile, call):
     if tile is not None:
         monkeypatch.setenv("QF8_TILE", str(tile))

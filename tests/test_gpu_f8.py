@@ -352,7 +352,7 @@ def test_gemm_few_rows(kind, M, N, K):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("M,N,K", [(0, 16, 64), (4, 0, 64), (3, 18, 0), (2, 140000, 0), (70000, 30, 0)])
+@pytest.mark.parametrize("M,N,K", [(0, 16, 64), (4, 0, 64), (3, 18, 0), (2, 140000, 0), (70000, 30, 0), (1100000, 3, 0)])
 def test_gemm_empty(kind, M, N, K):
     x = torch.zeros(M, K, dtype=XTYPE.get(kind, F16), device=DEV)
     xs = None
@@ -399,6 +399,25 @@ def test_gemm_every_kernel(monkeypatch, tile, kind, M, N, K):
         assert bool(torch.isnan(y[:, N // 2]).all())
         tol = sums(K, mag) + (left if yt == BF16 else 0.0)
         inside(y[:, torch.from_numpy(keep).to(DEV)], ref[:, keep], tol[:, keep])
+
+
+@pytest.mark.parametrize("tile", range(6))
+@pytest.mark.parametrize("kind", KINDS)
+def test_gemm_infinite_last_scale(monkeypatch, tile, kind):
+    # three blocks along K: two groups of waves share them unevenly, and the last scale is infinite
+    monkeypatch.setenv("QF8_TILE", str(tile))
+    rng = np.random.default_rng(tile)
+    M, N, K = 70, 40, 384
+    x, xs, xv = make_x(rng, kind, M, K)
+    wc, ws = random_f8(rng, N, K, 128)
+    ws[0, 2] = np.inf
+    wc[:, 256:] = 56                                        # 1.0: the last block's sum is x's
+    wc[:, 257:] = 0
+    x.view(torch.uint8 if kind == "f8" else torch.int16)[:, 256] &= 0x77 if kind == "f8" else 0x7777   # finite, its sign gone
+    keep = f64(x[:, 256].float()) > 0
+    for yt in (F32, BF16):
+        y = f64(qgm.f8_gemm(x, dev(wc), dev(ws), x_scales=xs, out_dtype=yt))
+        assert np.isposinf(y[keep]).all() and keep.sum() > 20
 
 
 @pytest.mark.parametrize("tile", range(6))
@@ -553,7 +572,7 @@ def test_gate_far_from_zero(act):
         assert (y == y[:, :1]).all() and (np.abs(y[:, 0] - ref) <= tol + stored(ref, F32)).all()
 
 
-@pytest.mark.parametrize("M,F,K", [(0, 16, 64), (4, 0, 64), (3, 32, 0), (70, 48, 0)])
+@pytest.mark.parametrize("M,F,K", [(0, 16, 64), (4, 0, 64), (3, 32, 0), (70, 48, 0), (1100000, 16, 0)])
 def test_gated_empty(M, F, K):
     x = torch.zeros(M, K, dtype=BF16, device=DEV)
     w = torch.zeros(2 * F, K, dtype=torch.uint8, device=DEV).view(CODE)
