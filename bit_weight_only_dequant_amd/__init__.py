@@ -706,17 +706,16 @@ def _f8_blocks(n):
 
 def _f8_matrix(codes, scales, what, dev, block=None):
     """(R, K, block) of a matrix of codes and scales; block: the one it must have."""
-    sh = codes.shape
-    if (codes.dtype is _CODE and scales.dtype is _F32 and len(sh) == 2 and sh[1] % 16 == 0
-            and codes.get_device() == dev and scales.get_device() == dev
+    sh, ss = codes.shape, scales.shape
+    if (codes.dtype is _CODE and scales.dtype is _F32 and len(sh) == 2 and len(ss) == 2 and sh[1] % 16 == 0
+            and ss[1] == (sh[1] + 127) >> 7 and codes.get_device() == dev and scales.get_device() == dev
             and codes.is_contiguous() and scales.is_contiguous()):
         R, K = sh
-        kb = _f8_blocks(K)
         if (R | K) >> 31:
             _mx_int(what, R, K)
-        if block != 1 and scales.shape == (_f8_blocks(R), kb):
+        if block != 1 and ss[0] == (R + 127) >> 7:
             return R, K, 128
-        if block != 128 and scales.shape == (R, kb):
+        if block != 128 and ss[0] == R:
             return R, K, 1
     rows = {1: "R", 128: "ceil(R/128)", None: "R or ceil(R/128)"}[block]
     raise ValueError(f"{what} must be contiguous {_CODE} codes [R, K], K a multiple of 16, and fp32 scales "

@@ -675,6 +675,10 @@ constexpr uint32_t PAST = 0x80000000u;   // an offset past every buffer's end
 // the groups' order.  (A stage of a small tile is a chain of waits that a single
 // group of waves cannot fill.)
 // W is the first operand: a lane's outputs run along a row of y.
+template <int XT, bool ROWS, int MI, int NI, int WM, int WN, int RING, int KG> constexpr int f8_tile_lds() {
+  constexpr int TM = 16 * MI * WM, TN = 16 * NI * WN;
+  return KG * RING * (TM * (XT == F8 ? 128 : 256) + TN * 128 + ((XT == F8 ? TM : 0) + (ROWS ? TN : 0)) * 4);
+}
 template <int XT, bool FAST, int MODE, bool ROWS, int MI, int NI, int WM, int WN, int RING, int KG>
 __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_eu(2))) void f8_tile_kernel(F8Args a, int tiles_m, int tiles_n) {
   constexpr int NW = WM * WN, TM = 16 * MI * WM, TN = 16 * NI * WN, TF = MODE == PRODUCT ? TN : TN / 2;
@@ -689,10 +693,13 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
   constexpr int SL = SROWS / 64 > 0 ? SROWS / 64 : 1, QS = (SROWS / 64 + NW - 1) / NW, QALL = QD + QS;   // such loads, and a wave's
   constexpr bool WHOLE = MI * NI <= (FAST ? 16 : 8);   // a stage's fragments are read during the one before (below)
   constexpr int PIECES = TM * XB + TN * 128, STAGE = PIECES + SROWS * 4;
+  static_assert(KG * RING * STAGE == f8_tile_lds<XT, ROWS, MI, NI, WM, WN, RING, KG>() && KG * RING * STAGE <= 160 * 1024, "LDS");
   static_assert(NW * 16 * (16 * NI + 4) * 4 <= RING * STAGE && (KG == 1 || 16 * (16 * NI + 4) <= MI * NI * 256),
                 "the strips of f8_store_as: a wave's lies within its own part of the sums");
-  // one array: with two, the compiler waits for every direct load before each read
-  __shared__ __align__(1024) uint8_t smem[KG * RING * STAGE];
+  // One array: with two, the compiler waits for every direct load before each read.  Its size is the launch's: where
+  // the compiler sees that one workgroup fills a CU, it gives its waves accumulation registers too, and moves the
+  // products out of them one by one.
+  extern __shared__ __align__(1024) uint8_t smem[];
   int tm, tn;
   if (!f8_tile(tiles_m, tiles_n, tm, tn)) return;
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
@@ -1143,9 +1150,10 @@ template <int XT, bool FAST, int MODE, bool ROWS, int TILE, int MI, int NI, int 
 void launch_tiles(const F8Args& a, hipStream_t s) {
   constexpr F8Tile t = F8_TILES[FAST ? KIND_FAST : XT == F8 ? KIND_EXACT : KIND_16][TILE - 1];
   static_assert(t.rows == 16 * MI * WM && t.cols == 16 * NI * WN && t.waves == WM * WN, "as planned");
+  constexpr size_t lds = f8_tile_lds<XT, ROWS, MI, NI, WM, WN, RING, t.groups>();
   const dim3 grid((unsigned)f8_grid(a.M, a.w_rows, t));
   hipLaunchKernelGGL((f8_tile_kernel<XT, FAST, MODE, ROWS, MI, NI, WM, WN, RING, t.groups>), grid, dim3(t.waves * t.groups * 64),
-                     0, s, a, (a.M + t.rows - 1) / t.rows, (int)(((int64_t)a.w_rows + t.cols - 1) / t.cols));
+                     lds, s, a, (a.M + t.rows - 1) / t.rows, (int)(((int64_t)a.w_rows + t.cols - 1) / t.cols));
 }
 
 template <int XT, bool FAST, int MODE, bool ROWS> void launch_f8(const F8Args& a, const F8Plan& p, hipStream_t s) {
