@@ -682,3 +682,33 @@ def test_another_stream_and_graph_replays(kind, M):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, all_of(*other)))
+
+
+def test_two_streams_at_once():
+    # nothing is shared between calls: two sets on two streams, many times over
+    sets = [small_set("f8", 300, F=272, K=1040, seed=1), small_set("bf16", 5, F=48, K=272, seed=2)]
+    want = [all_of(*s) for s in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(all_of(*sets[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, want[i]))
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_rows_of_a_padded_batch_stand_alone(M):
+    # rows behind the last sequence hold anything: the others are as without them
+    x, xs, w, ws, dh = small_set("bf16", M + 9, F=64, K=400)
+    clean = x.clone()
+    x[M:] = float("nan")
+    dh2 = dh.clone()
+    dh2[M:] = float("inf")
+    for got, want in ((qgm.f8_gemm(x, w, ws), qgm.f8_gemm(clean, w, ws)), (qgm.f8_gated(x, w, ws), qgm.f8_gated(clean, w, ws)),
+                      (qgm.f8_gated_grad(dh2, x, w, ws), qgm.f8_gated_grad(dh, clean, w, ws)),
+                      (qgm.f8_quantize(x)[0][:M].view(torch.uint8), qgm.f8_quantize(clean)[0][:M].view(torch.uint8))):
+        assert torch.equal(got[:M], want[:M])
