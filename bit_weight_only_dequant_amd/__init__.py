@@ -806,7 +806,9 @@ def f8_gemm(x, w, w_scales, x_scales=None, out=None, out_dtype=None, residual=No
     x: fp16 or bf16 [M, K] with unit column stride, or E4M3 codes with x_scales
     [M, ceil(K/128)]; w_scales in blocks of 128 x 128, or with 8-bit x [N,
     ceil(K/128)] too.  y: out_dtype (fp16, bf16 or fp32; x's type by default,
-    fp16 for 8-bit x); see qf8_gemm."""
+    fp16 for 8-bit x).  bf16 results of 8-bit x and blocks of 128 x 128 may come
+    from 8-bit matrix instructions, which lose up to 7 * 2^-13 of the largest
+    product of every 8 k; fp16 and fp32 results do not.  See qf8_gemm."""
     ctx = _mx_elsewhere(x, stream)
     if ctx is not None:
         with ctx:

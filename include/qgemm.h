@@ -470,10 +470,15 @@ int qf8_dequantize(const uint8_t* codes, const float* scales, int block, int M, 
  *   residual [device, in] y_type [M, N] with leading dimension ldr >= N, or NULL.  It may be y
  *            itself when ldr == ldy.
  *   y        [device, out] y_type QG_MX_F16, QG_MX_BF16 or QG_MX_F32, leading dimension ldy >= N.
- * Precision.  Products of codes with codes converted to 16 bits, and of those with 16-bit x, are exact in fp32.  With
- * 8-bit x, w_block 128 and bf16 results of more than a few rows, 8-bit matrix instructions multiply: they add the
- * products of 8 consecutive k on a grid of 2^(e - 13), e the largest sum of two codes' exponents among them, and cut
- * what is finer, which is about a tenth of the result's own rounding.
+ * Precision.  With 16-bit x, with w_block 1 and with QG_MX_F16 or QG_MX_F32 results the products of converted codes
+ * are exact in fp32, and the sums are fp32's.  With 8-bit x, w_block 128 and QG_MX_BF16 results the kernel for few
+ * rows works so too, and the others (qf8_plan's out[0] > 0) use 8-bit matrix instructions.  Of every 8 consecutive k
+ * those add the products on a grid of 2^(e - 13), e the largest sum of two codes' exponents among the 8 (a subnormal
+ * code's is -6), and cut what is finer: up to 7 * 2^-13 of the largest |code of x| times the largest |code of w| of
+ * the 8 (each at least 2^-6), times the scales.  That is relative to the terms and not to the result: with random
+ * operands it is about a tenth of bf16's own rounding, but where large products cancel, what is left of the 8 may
+ * be lost (256 * 256 - 256 * 256 + 6 * 1.75 * 4 gives 0 for 42).  The same row may differ by as much between a batch
+ * of a few rows and a larger one.  A caller who wants exact products takes fp32 or fp16 results.
  * M == 0 or N == 0 is a no-op; K == 0 writes zeros (plus the residual).
  * Sums are added in a fixed order: equal inputs give equal bits.
  * Errors: QG_E_ARG, QG_E_ALIGN, QG_E_UNSUPPORTED (sizes beyond 2^31 - 513; more pieces of y than a grid
@@ -486,7 +491,7 @@ int qf8_gemm(const void* x, int ldx, int x_type, const float* x_scales, const ui
 /*
  * qf8_gated: h[M, F] = act(x . Wg^T) * (x . Wu^T), both projections, the
  * activation and the product in one kernel.  Neither projection is rounded or
- * written to memory.
+ * written to memory; their sums are as precise as qf8_gemm's for h_type.
  *   x, x_scales as qf8_gemm.
  *   w, w_scales [device, in] [2F, K] in blocks of 128: Wg is its first F rows, Wu the others.  F % 16 == 0 (a
  *            block may hold rows of both).

@@ -712,3 +712,47 @@ def test_rows_of_a_padded_batch_stand_alone(M):
                       (qgm.f8_gated_grad(dh2, x, w, ws), qgm.f8_gated_grad(dh, clean, w, ws)),
                       (qgm.f8_quantize(x)[0][:M].view(torch.uint8), qgm.f8_quantize(clean)[0][:M].view(torch.uint8))):
         assert torch.equal(got[:M], want[:M])
+
+
+# ---------------------------------------- the ends of precision, range and pitch
+
+@pytest.mark.parametrize("tile", range(6))
+def test_large_products_cancel_within_eight(monkeypatch, tile):
+    # 256 * 256 - 256 * 256 + 6 * 7 in every eight of w, one eight of each row of x: 42 times the scales.  Converted codes
+    # give it exactly (every partial sum is an integer below 2^24); the 8-bit matrix instructions may cut up to 7 * 2^3
+    # of it, as documented, so nothing of it need be left.
+    monkeypatch.setenv("QF8_TILE", str(tile))
+    M, N, K = 70, 64, 144
+    xv, wv = np.zeros((M, K), np.float32), np.tile(np.array([256, 256] + [4] * 6, np.float32), (N, K // 8))
+    for m in range(M):
+        at = 8 * (m % (K // 8))
+        xv[m, at:at + 8] = [256, -256] + [1.75] * 6
+    xc, wc = (torch.from_numpy(v).to(CODE).view(torch.uint8).numpy() for v in (xv, wv))
+    rng = np.random.default_rng(tile)
+    xsn = np.exp2(rng.integers(-3, 4, (M, 2))).astype(np.float32)
+    ws = np.exp2(rng.integers(-8, -4, (1, 2))).astype(np.float32)
+    x, xs = dev(xc), dev(xsn)
+    xd, wd = f8ref.f8_values(xc, xsn), f8ref.f8_values(wc, ws)
+    ref, mag = f8ref.f8_gemm_ref(xd, wd)
+    left = cut(x, xs, wc, ws, BF16)
+    assert (ref == 42 * np.take_along_axis(xsn * ws, (np.arange(M) % (K // 8) // 16)[:, None], 1)).all()
+    assert (left >= ref).all() and (left <= 57 * xsn.max(1, keepdims=True) * ws.max()).all()
+    for yt in (F32, F16):
+        assert np.array_equal(f64(qgm.f8_gemm(x, dev(wc), dev(ws), x_scales=xs, out_dtype=yt)), rounded(ref, yt))
+    y = qgm.f8_gemm(x, dev(wc), dev(ws), x_scales=xs, out_dtype=BF16)
+    inside(y, ref, sums(K, mag) + left)
+    few = qgm.f8_gemm(x[:3], dev(wc), dev(ws), x_scales=xs[:3], out_dtype=BF16)
+    inside(few, ref[:3], sums(K, mag[:3]) + left[:3])
+    if tile == 0:   # the kernel for few rows converts the codes
+        assert np.array_equal(f64(y), rounded(ref, BF16))
+    # the gated forms: their projections are off by as much
+    for act in ACTS:
+        for yt in (BF16, F32):
+            h, tol, (g, u, a, da, eg, eu, ea, t) = gate_tolerances(xd, wd, act, K, cut(x, xs, wc, ws, yt))
+            inside(qgm.f8_gated(x, dev(wc), dev(ws), x_scales=xs, act=act, out_dtype=yt), h, tol)
+            dh = torch.ones(M, N // 2, dtype=yt, device=DEV)
+            s = np.where(g != 0, a / np.where(g != 0, g, 1), 0.5)
+            es = (8 * t + 16) * U * (np.abs(s) + np.abs(da - s)) + 2.0 ** -126 * (1 + np.abs(g)) + eg
+            want = f8ref.gated_grad_ref(f64(dh), xd, wd, act)
+            tol = np.concatenate([es * np.abs(u) + (np.abs(da) + es) * eu, ea], axis=1) + 2 * U * np.abs(want)
+            inside(qgm.f8_gated_grad(dh, x, dev(wc), dev(ws), x_scales=xs, act=act), want, tol)
