@@ -855,7 +855,10 @@ def f8_gated_grad(dh, x, w, w_scales, x_scales=None, act="silu", out=None, strea
     """The gradients of f8_gated's projections from dh [M, F] (fp16, bf16 or fp32,
     unit column stride): d [M, 2F] of dh's type, dh * u * act'(g) beside dh *
     act(g), with g and u computed again from x and w as f8_gated takes them.
-    The input's gradient is f8_gemm(d, w transposed); see qf8_gated_grad."""
+    The input's gradient is f8_gemm(d, w transposed).  A 16-bit d is rounded
+    before that product; from fp32 dh, and so d, the input's gradient without
+    that rounding is the sum of two (residual=) of d.to(torch.bfloat16) and of
+    what that leaves; see qf8_gated_grad."""
     ctx = _mx_elsewhere(x, stream)
     if ctx is not None:
         with ctx:

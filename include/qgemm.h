@@ -508,7 +508,11 @@ int qf8_gated(const void* x, int ldx, int x_type, const float* x_scales, const u
  *   d[:, 0:F] = dh * u * act'(g),   d[:, F:2F] = dh * act(g).
  * The gradients follow from d [M, 2F] as products: dx = d . W (qf8_gemm with
  * the transposed weight), dW = d^T . x (qf8_gemm of both operands quantised with
- * transpose = 1).
+ * transpose = 1).  d is rounded once, to d_type; of a 16-bit d, dx and dW carry that
+ * rounding beside their own (bf16: dx is off by 1.4 times as much as from a d that is
+ * not rounded).  For more, take dh and d in fp32 and dx as two products, of d
+ * rounded to bf16 and of what that leaves, the first (in fp32) the residual of the
+ * second: together within 2^-16 of d's.
  *   dh       [device, in] d_type [M, F], leading dimension lddh >= F.
  *   x, x_scales, w, w_scales, act as qf8_gated.
  *   d        [device, out] d_type [M, 2F], leading dimension ldd >= 2F; not dh's memory.

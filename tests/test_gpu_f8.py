@@ -756,3 +756,28 @@ def test_large_products_cancel_within_eight(monkeypatch, tile):
             want = f8ref.gated_grad_ref(f64(dh), xd, wd, act)
             tol = np.concatenate([es * np.abs(u) + (np.abs(da) + es) * eu, ea], axis=1) + 2 * U * np.abs(want)
             inside(qgm.f8_gated_grad(dh, x, dev(wc), dev(ws), x_scales=xs, act=act), want, tol)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M", [3, 150])
+def test_input_gradient_without_rounding_between(kind, M):
+    # d in fp32 and its product with the weights turned over as two: of d rounded to bf16, and of what that leaves,
+    # rounded too.  What both leave is at most 2^-8 2^-8 of d, so dx is that of the unrounded d within 2^-16.
+    rng = np.random.default_rng(M)
+    F, K = 80, 272
+    x, xs, xv = make_x(rng, kind, M, K)
+    wc, ws = random_f8(rng, 2 * F, K, 128, size=0.02 if kind != "f8" else 0.005)
+    wv = f8ref.f8_values(wc, ws)
+    back = qgm.F8Linear(dev(wc.T), dev(ws.T))
+    dh = torch.randn(M, F, device=DEV)
+    d = qgm.f8_gated_grad(dh, x, dev(wc), dev(ws), x_scales=xs)
+    assert d.dtype == F32
+    high = d.to(BF16)
+    dx = back(high, out_dtype=F32)
+    back((d - high.float()).to(BF16), out=dx, residual=dx)
+    ref, mag = f8ref.f8_gemm_ref(f64(d), wv.T)
+    inside(dx, ref, (2.0 ** -16 + 2 * sums(2 * F, 1)) * mag)
+    # and of the formula's: half a step of bf16 in d alone would be 2^-8 of each term
+    want = f8ref.gated_grad_ref(f64(dh), xv, wv, "silu") @ wv
+    gap = np.linalg.norm(f64(dx) - want) / np.linalg.norm(want)
+    assert gap < 2.0 ** -15, gap
