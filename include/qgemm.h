@@ -479,6 +479,10 @@ int qf8_dequantize(const uint8_t* codes, const float* scales, int block, int M, 
  * operands it is about a tenth of bf16's own rounding, but where large products cancel, what is left of the 8 may
  * be lost (256 * 256 - 256 * 256 + 6 * 1.75 * 4 gives 0 for 42).  The same row may differ by as much between a batch
  * of a few rows and a larger one.  A caller who wants exact products takes fp32 or fp16 results.
+ * Range.  The two scales of a block are multiplied before they meet its sum (with 16-bit x there is one).  Their
+ * product has to be a normal fp32 number (2^-126 to 2^128), and the block's sum, without the scales and times them,
+ * below 2^128.  Outside, a block gives infinities or NaN (zero codes under scales of 2^64 and 2^64: 0 * infinity) or
+ * loses bits, even where its value is within fp32.  qf8_quantize's scales lie between 2^-109 and 2^120.
  * M == 0 or N == 0 is a no-op; K == 0 writes zeros (plus the residual).
  * Sums are added in a fixed order: equal inputs give equal bits.
  * Errors: QG_E_ARG, QG_E_ALIGN, QG_E_UNSUPPORTED (sizes beyond 2^31 - 513; more pieces of y than a grid

@@ -781,3 +781,45 @@ def test_input_gradient_without_rounding_between(kind, M):
     want = f8ref.gated_grad_ref(f64(dh), xv, wv, "silu") @ wv
     gap = np.linalg.norm(f64(dx) - want) / np.linalg.norm(want)
     assert gap < 2.0 ** -15, gap
+
+
+@pytest.mark.parametrize("tile", range(6))
+@pytest.mark.parametrize("kind", KINDS + ["rows"])
+@pytest.mark.parametrize("end", ["low", "high", "mixed"])
+def test_gemm_ends_of_the_scales_range(monkeypatch, tile, kind, end):
+    # factors of a block (the product of its two scales; with 16-bit x the one) from 2^-126 on, and sums up to 2^127:
+    # what is documented to be as good as elsewhere, but for results below 2^-126, which are multiples of 2^-149
+    monkeypatch.setenv("QF8_TILE", str(tile))
+    rng = np.random.default_rng(tile)
+    M, N, K = 70, 66, 304
+    x, xs, xv = make_x(rng, "f8" if kind == "rows" else kind, M, K)
+    wc, ws = random_f8(rng, N, K, 1 if kind == "rows" else 128)
+    xe, we = {"low": (-80, -46), "high": (70, 30), "mixed": (119, -108)}[end]
+    if xs is None:
+        ex = 8 if kind == "f16" else {"low": 0, "high": 90, "mixed": 110}[end]
+        x = x * 2.0 ** ex
+        xv, we = f64(x), {"low": -126, "high": 108 - ex, "mixed": 0 - ex}[end]
+    else:
+        xs = dev((rng.uniform(1, 2, tuple(xs.shape)) * 2.0 ** xe).astype(np.float32))
+        xv = f8ref.f8_values(codes_of(x), xs.cpu().numpy())
+    ws = (rng.uniform(1, 2, ws.shape) * 2.0 ** we).astype(np.float32)
+    ref, mag = f8ref.f8_gemm_ref(xv, f8ref.f8_values(wc, ws))
+    assert mag.max() < 2.0 ** 127
+    for yt in (F32, BF16):
+        y = qgm.f8_gemm(x, dev(wc), dev(ws), x_scales=xs, out_dtype=yt)
+        inside(y, ref, sums(K, mag) + cut(x, xs, wc, ws, yt) + 4 * 2.0 ** -149)
+
+
+@pytest.mark.parametrize("tile", range(6))
+@pytest.mark.parametrize("kind,least", [("f16", 2.0 ** -24), ("bf16", 2.0 ** -133)])
+def test_gemm_subnormal_x(monkeypatch, tile, kind, least):
+    # multiples of the type's smallest number count in full
+    monkeypatch.setenv("QF8_TILE", str(tile))
+    rng = np.random.default_rng(tile)
+    M, N, K = 70, 66, 176
+    n = rng.integers(-64, 65, (M, K))
+    x = torch.from_numpy(n * least).to(XTYPE[kind]).to(DEV)
+    wc, ws = exact_f8(rng, N, K, 128)
+    ws *= 2.0 ** 20
+    ref, _ = f8ref.f8_gemm_ref(n * least, f8ref.f8_values(wc, ws))
+    assert np.array_equal(f64(qgm.f8_gemm(x, dev(wc), dev(ws), out_dtype=F32)), ref) and ref.any()
