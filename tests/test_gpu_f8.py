@@ -823,3 +823,30 @@ def test_gemm_subnormal_x(monkeypatch, tile, kind, least):
     ws *= 2.0 ** 20
     ref, _ = f8ref.f8_gemm_ref(n * least, f8ref.f8_values(wc, ws))
     assert np.array_equal(f64(qgm.f8_gemm(x, dev(wc), dev(ws), out_dtype=F32)), ref) and ref.any()
+
+
+@pytest.mark.parametrize("more", [0, 8])
+@pytest.mark.parametrize("tile", [None, 0, 1, 2, 3, 4, 5])
+def test_widest_pitch_of_x(monkeypatch, tile, more):
+    # rows of x 4 MiB apart, the most that the tiles' 32-bit buffers take, and 16 bytes further, which the kernel for
+    # few rows takes whatever is forced: more rows than its 16, several tiles, NaN between them
+    if tile is not None:
+        monkeypatch.setenv("QF8_TILE", str(tile))
+    rng = np.random.default_rng(7)
+    M, F, K = 270, 48, 80
+    xt, _, xv = make_x(rng, "bf16", M, K)
+    wide = torch.full((M, (1 << 21) + more), float("nan"), dtype=BF16, device=DEV)
+    wide[:, :K] = xt
+    x = wide[:, :K]
+    wc, ws = random_f8(rng, 2 * F, K, 128, size=0.02)
+    w, s = dev(wc), dev(ws)
+    ref, mag = f8ref.f8_gemm_ref(xv, f8ref.f8_values(wc, ws))
+    y = qgm.f8_gemm(x, w, s, out_dtype=F32)
+    inside(y, ref, sums(K, mag))
+    h, tol, _ = gate_tolerances(xv, f8ref.f8_values(wc, ws), "silu", K)
+    inside(qgm.f8_gated(x, w, s, out_dtype=F32), h, tol)
+    dh = torch.ones(M, F, device=DEV)
+    d = qgm.f8_gated_grad(dh, x, w, s)
+    if more:   # the same kernel as for rows without gaps: the same bits
+        monkeypatch.setenv("QF8_TILE", "0")
+    assert torch.equal(y, qgm.f8_gemm(xt, w, s, out_dtype=F32)) and torch.equal(d, qgm.f8_gated_grad(dh, xt, w, s))
