@@ -692,7 +692,9 @@ class MXLinear:
 # 8-bit floating point (E4M3) with an fp32 scale for blocks of 128: codes
 # torch.float8_e4m3fn [R, K] and scales fp32 [R, ceil(K/128)] (block 1) or
 # [ceil(R/128), ceil(K/128)] (block 128), both contiguous, K a multiple of 16;
-# see include/qgemm.h.
+# see include/qgemm.h.  As everywhere in this module results carry no autograd
+# graph, whatever requires a gradient among the inputs: a program that trains
+# calls f8_gated_grad and the products in its own torch.autograd.Function.
 
 F8_E4M3 = 4
 F8_BLOCK = 128
@@ -889,7 +891,8 @@ def f8_plan(M: int, N: int, K: int, x_type: int, y_type: int = MX_BF16, w_block:
 
 class F8Linear:
     """One weight matrix [N, K] in E4M3 with blocks of 128 x 128 on the GPU: the
-    8-bit sibling of QuantLinear and MXLinear."""
+    8-bit sibling of QuantLinear and MXLinear.  Results carry no autograd graph;
+    the backward pass is F8Linear.from_weight(weight, transpose=True)."""
 
     def __init__(self, codes, scales):
         _dev(codes, "codes")
@@ -910,7 +913,8 @@ class F8Linear:
 
 class F8Gated:
     """The gate and up projections [2F, K] of a feed-forward block in E4M3, with
-    its activation."""
+    its activation.  Results carry no autograd graph: grad() is the backward
+    pass, which the program calls."""
 
     def __init__(self, codes, scales, act="silu"):
         _dev(codes, "codes")

@@ -850,3 +850,31 @@ def test_widest_pitch_of_x(monkeypatch, tile, more):
     if more:   # the same kernel as for rows without gaps: the same bits
         monkeypatch.setenv("QF8_TILE", "0")
     assert torch.equal(y, qgm.f8_gemm(xt, w, s, out_dtype=F32)) and torch.equal(d, qgm.f8_gated_grad(dh, xt, w, s))
+
+
+def test_results_carry_no_graph():
+    # the operators are not joined to autograd; a program that trains wraps them in a function of its own
+    x, xs, w, ws, dh = small_set("bf16", 5, F=48, K=272)
+    block, back = qgm.F8Gated(w, ws), qgm.F8Linear(w.view(torch.uint8).t().contiguous().view(CODE), ws.t().contiguous())
+
+    class Gated(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            ctx.save_for_backward(x)
+            return block(x)
+
+        @staticmethod
+        def backward(ctx, dh):
+            return back(block.grad(dh, *ctx.saved_tensors))
+
+    x.requires_grad_()
+    assert not block(x).requires_grad and not back(block.grad(dh, x)).requires_grad
+    h = Gated.apply(x)
+    got, = torch.autograd.grad(h, x, dh)
+    assert torch.equal(h, block(x)) and torch.equal(got, back(block.grad(dh, x)))
+    wv = torch.from_numpy(f8ref.f8_values(codes_of(w), ws.cpu().numpy())).to(DEV)
+    xd = x.detach().double().requires_grad_()
+    p = xd @ wv.t()
+    want, = torch.autograd.grad(torch.nn.functional.silu(p[:, :48]) * p[:, 48:], xd, dh.double())
+    gap = (got.double() - want).norm() / want.norm()
+    assert gap < 2.0 ** -7, gap   # d and dx rounded once each, by half a step (2^-8) at most
