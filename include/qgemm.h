@@ -498,10 +498,11 @@ int qf8_gemm(const void* x, int ldx, int x_type, const float* x_scales, const ui
  * written to memory; their sums are as precise as qf8_gemm's for h_type.
  *   x, x_scales as qf8_gemm.
  *   w, w_scales [device, in] [2F, K] in blocks of 128: Wg is its first F rows, Wu the others.  F % 16 == 0 (a
- *            block may hold rows of both).
+ *            block may hold rows of both), F <= 2^30 - 513 (2F rows are numbered in 32 bits).
  *   act      qg_act_t.
  *   h        [device, out] h_type QG_MX_F16, QG_MX_BF16 or QG_MX_F32, leading dimension ldh >= F.
- * M == 0 or F == 0 is a no-op; K == 0 writes zeros.  Errors as qf8_gemm.
+ * M == 0 or F == 0 is a no-op; K == 0 writes zeros.  Errors as qf8_gemm; an F that is no multiple of 16 or
+ * beyond its limit is QG_E_ARG.
  */
 int qf8_gated(const void* x, int ldx, int x_type, const float* x_scales, const uint8_t* w, const float* w_scales,
               int act, int M, int F, int K, void* h, int ldh, int h_type, void* stream);
@@ -520,7 +521,7 @@ int qf8_gated(const void* x, int ldx, int x_type, const float* x_scales, const u
  *   dh       [device, in] d_type [M, F], leading dimension lddh >= F.
  *   x, x_scales, w, w_scales, act as qf8_gated.
  *   d        [device, out] d_type [M, 2F], leading dimension ldd >= 2F; not dh's memory.
- * M == 0 or F == 0 is a no-op.  Errors as qf8_gemm.
+ * M == 0 or F == 0 is a no-op.  Errors as qf8_gated.
  */
 int qf8_gated_grad(const void* dh, int lddh, const void* x, int ldx, int x_type, const float* x_scales,
                    const uint8_t* w, const float* w_scales, int act, int M, int F, int K, void* d, int ldd,
@@ -531,7 +532,8 @@ int qf8_gated_grad(const void* dh, int lddh, const void* x, int ldx, int x_type,
  * out[0] = 0 the kernel for few rows, 1..4 the tiled kernel on 64 x 64, 64 x 128, 128 x 128 or 256 x 256 (128 x 256 unless
  * 8-bit matrix instructions are used: 8-bit x, w_block 128 and y_type QG_MX_BF16) outputs, gated forms half as many
  * features, 5 on 64 x 64 with two groups of waves; out[1] = waves a workgroup of the first; out[2] = pieces of y.
- * QF8_TILE=0..5 in the environment forces out[0].  Errors: QG_E_ARG, QG_E_UNSUPPORTED (as the products, by the sizes). */
+ * QF8_TILE=0..5 in the environment forces out[0].  Errors: QG_E_ARG, QG_E_UNSUPPORTED (sizes beyond 2^31 - 513, or
+ * features beyond 2^30 - 513; whether a grid holds the pieces is the products' to say). */
 int qf8_plan(int gated, int M, int N, int K, int x_type, int y_type, int w_block, int out[3]);
 
 /*

@@ -196,6 +196,16 @@ def test_grad_refuses(kw, expect):
     assert grad(**kw) == expect
 
 
+def test_features_up_to_their_limit():
+    # 2^30 - 513 features at most: the largest multiple of 16 below it goes on, the next is refused by name
+    last, out = (1 << 30) - 528, (qgm.ctypes.c_int * 3)()
+    for call in (gated, grad):
+        assert call(N=last + 16) == E_ARG and call(N=last + 16, xt=F8, xs=A) == E_ARG
+        assert call(N=last, M=0) == OK and call(N=last, ldy=16) == E_ARG and call(N=last, w=A + 4) == E_ALIGN
+    assert lib.qf8_plan(1, 2, last, 64, F16, F16, 128, out) == OK and out[2] > 0
+    assert lib.qf8_plan(1, 2, last + 16, 64, F16, F16, 128, out) == E_UNSUP
+
+
 @pytest.mark.skipif(gpu_present(), reason="checks the no-device status; a GPU is present")
 def test_no_device_status():
     assert quantize() == E_DEVICE and quantize(block=128, turn=1) == E_DEVICE and dequantize() == E_DEVICE
