@@ -413,7 +413,7 @@ __global__ __launch_bounds__(NW * 64) void f8_rows_kernel(F8Args a) {
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int np = a.K >> 4;                        // 16-byte pieces of a row of codes
-  const int chunks = (np + 31) >> 5, turns = (chunks + NW - 1) / NW;   // a wave's chunks: wave, wave + NW, ..
+  const int chunks = (np + 31) >> 5, turns = (chunks + NW - 1) / NW;   // (at least one) a wave's chunks: wave, wave + NW, ..
   const int blocks = MODE == PRODUCT ? (a.N + 15) >> 4 : a.F >> 4;
   const int m0 = blockIdx.y * 16, rows = min(a.M - m0, 16), rr = min(r, rows - 1);
   const int xbytes = f8_x_bytes<XT>(a.M);
@@ -466,10 +466,11 @@ __global__ __launch_bounds__(NW * 64) void f8_rows_kernel(F8Args a) {
   S s;
   f4 acc[NT];
   int nb = blockIdx.x, turn = 0, buf = 0;
-  if (chunks > 0) {
-    if (turns == 1 && wave < chunks) load_x(wave);
-    load_w(nb, min(wave, chunks - 1), w0);
-  }
+  // The first loads go out before anything that follows is begun (mixed with it: 1 x 6144 x 2048 5.75 us instead of 5.65).
+  __builtin_amdgcn_sched_barrier(0);
+  if (turns == 1 && wave < chunks) load_x(wave);
+  load_w(nb, min(wave, chunks - 1), w0);
+  __builtin_amdgcn_sched_barrier(0);
   // one chunk of one block: its products, and after a block's last chunk the sums
   auto item = [&](auto MORE, W& w, W& next) {   // MORE: another item follows
     const int c = wave + turn * NW;
@@ -561,7 +562,7 @@ __global__ __launch_bounds__(NW * 64) void f8_rows_kernel(F8Args a) {
     turn = 0;
     nb += gridDim.x;
   };
-  int left = nb < blocks ? ((blocks - 1 - nb) / (int)gridDim.x + 1) * max(turns, 1) : 0;
+  int left = nb < blocks ? ((blocks - 1 - nb) / (int)gridDim.x + 1) * turns : 0;
   if constexpr (MULTI) {
     for (; left > 2; left -= 2) {
       item(std::true_type{}, w0, w1);
@@ -1062,8 +1063,9 @@ template <int MODE, int YT> __global__ __launch_bounds__(EW_THREADS) void f8_no_
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-// Which kernel takes a product.  tile 0: f8_rows_kernel with nw waves a workgroup; 1..5: f8_tile_kernel on F8_TILES.
-// QF8_TILE=0..5 in the environment forces one (tests, tuning).  fits: whether a grid holds it.
+// Which kernel takes a product.  tile 0: f8_rows_kernel with nw waves a workgroup (without a k f8_no_k_kernel); 1..5:
+// f8_tile_kernel on F8_TILES.  QF8_TILE=0..5 in the environment forces one where there is a choice, with a k and rows
+// of x of up to 4 MiB (tests, tuning).  fits: whether a grid holds it.
 struct F8Plan { int tile, nw; int64_t workgroups; bool fits; };
 
 // What the tiles multiply with: 16-bit x, 8-bit x on converted codes, 8-bit x as it is.

@@ -532,7 +532,9 @@ int qf8_gated_grad(const void* dh, int lddh, const void* x, int ldx, int x_type,
  * out[0] = 0 the kernel for few rows, 1..4 the tiled kernel on 64 x 64, 64 x 128, 128 x 128 or 256 x 256 (128 x 256 unless
  * 8-bit matrix instructions are used: 8-bit x, w_block 128 and y_type QG_MX_BF16) outputs, gated forms half as many
  * features, 5 on 64 x 64 with two groups of waves; out[1] = waves a workgroup of the first; out[2] = pieces of y.
- * QF8_TILE=0..5 in the environment forces out[0].  Errors: QG_E_ARG, QG_E_UNSUPPORTED (sizes beyond 2^31 - 513, or
+ * K == 0 has out[0] = 0 and out[1] = 1; an elementwise kernel writes it.
+ * QF8_TILE=0..5 in the environment forces out[0], but for K == 0 and rows of x of more than 4 MiB (with their gaps):
+ * those are always 0.  Errors: QG_E_ARG, QG_E_UNSUPPORTED (sizes beyond 2^31 - 513, or
  * features beyond 2^30 - 513; whether a grid holds the pieces is the products' to say). */
 int qf8_plan(int gated, int M, int N, int K, int x_type, int y_type, int w_block, int out[3]);
 

@@ -326,6 +326,22 @@ def test_plans(monkeypatch):
         assert lib.qf8_plan(*bad, out) == E_UNSUP
 
 
+@pytest.mark.parametrize("forced", [None, 0, 1, 4, 5])
+def test_plans_without_a_choice(monkeypatch, forced):
+    # nothing to multiply, or rows of x of more than 4 MiB: the setting is not asked
+    if forced is not None:
+        monkeypatch.setenv("QF8_TILE", str(forced))
+    for gated_ in (False, True):
+        for M in (1, 40, 5000):
+            for x_type in (F16, BF16, F8):
+                assert qgm.f8_plan(M, 304, 0, x_type, gated=gated_)["tile"] == 0
+                assert qgm.f8_plan(M, 304, 0, x_type, gated=gated_)["waves"] == 1
+                assert qgm.f8_plan(M, 304, (1 << 22) + 16, x_type, gated=gated_)["tile"] == 0
+            assert qgm.f8_plan(M, 304, (1 << 21) + 16, BF16, gated=gated_)["tile"] == 0
+    if forced is not None:
+        assert qgm.f8_plan(40, 304, 1 << 21, BF16)["tile"] == forced == qgm.f8_plan(40, 304, 1 << 22, F8)["tile"]
+
+
 @pytest.mark.parametrize("M,N", [(0, 16), (16, 0), (0, 0)])
 def test_plan_of_nothing(M, N):
     for K in (0, 64, 8192):
