@@ -23,10 +23,8 @@ typedef bf16 b2 __attribute__((ext_vector_type(2)));
 typedef bf16 b8 __attribute__((ext_vector_type(8)));
 typedef float f2 __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef int i8v __attribute__((ext_vector_type(8)));
-typedef float f16v __attribute__((ext_vector_type(16)));
 
 constexpr int F16 = QG_MX_F16, BF16 = QG_MX_BF16, F32 = QG_MX_F32;
 
@@ -92,37 +90,6 @@ template <int C, typename E> __device__ __forceinline__ void put(E* p, const E (
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(f16 v) { return (float)v; }
 __device__ __forceinline__ float to_f32(bf16 v) { return bits_f32((uint32_t)__builtin_bit_cast(uint16_t, v) << 16); }
-
-// C (4 or 8) consecutive outputs of one row, columns n .. n+C-1 of row m: the
-// factor and the residual in fp32, one rounding.  Rows of any pitch are stored
-// in one piece (the device takes vector accesses at element alignment).  Args has
-// y, ldy, y_type, N, resid (or NULL) and ldr.
-template <int YT, int C, typename Args> __device__ __forceinline__ void store_cols_as(const Args& a, int m, int n, float (&v)[C], float factor) {
-  typedef typename Elem<YT>::type E;
-  const bool whole = n + C <= a.N;
-  const int have = min(a.N - n, C);
-#pragma unroll
-  for (int i = 0; i < C; ++i) v[i] *= factor;
-  if (a.resid) {
-    E r[C] = {};
-    const E* rp = reinterpret_cast<const E*>(a.resid) + (int64_t)m * a.ldr + n;
-    if (whole) get(rp, r);
-    else for (int i = 0; i < C; ++i) if (i < have) r[i] = rp[i];
-#pragma unroll
-    for (int i = 0; i < C; ++i) v[i] += to_f32(r[i]);
-  }
-  E q[C];
-#pragma unroll
-  for (int i = 0; i < C; ++i) q[i] = (E)v[i];
-  E* y = reinterpret_cast<E*>(a.y) + (int64_t)m * a.ldy + n;
-  if (whole) put(y, q);
-  else for (int i = 0; i < C; ++i) if (i < have) y[i] = q[i];
-}
-template <int C, typename Args> __device__ __forceinline__ void store_cols(const Args& a, int m, int n, float (&v)[C], float factor) {
-  if (a.y_type == F32) store_cols_as<F32, C>(a, m, n, v, factor);
-  else if (a.y_type == F16) store_cols_as<F16, C>(a, m, n, v, factor);
-  else store_cols_as<BF16, C>(a, m, n, v, factor);
-}
 
 typedef const void __attribute__((address_space(1)))* gptr;
 typedef void __attribute__((address_space(3)))* lptr;

@@ -36,6 +36,8 @@
 namespace qg {
 namespace {
 
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
 constexpr int F8 = QG_F8_E4M3;
 constexpr float F8_TOP = 448.f;                 // the largest code
 constexpr float F8_LOWEST = 0x1p-100f;          // a block's largest magnitude counts as at least this

@@ -44,6 +44,8 @@
 namespace qg {
 namespace {
 
+typedef float f16v __attribute__((ext_vector_type(16)));
+
 constexpr int FP4 = QG_MX_FP4;
 
 // The E8M0 byte s as the conversions take their scale: the exponent field of
@@ -193,6 +195,36 @@ template <int S> __device__ __forceinline__ f16v mfma_fp4_32(u4 a, uint32_t sa, 
   const i8v av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
   const i8v bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, S, (int)sa, S, (int)sb);
+}
+
+// C (4 or 8) consecutive outputs of one row, columns n .. n+C-1 of row m: the
+// factor and the residual in fp32, one rounding.  Rows of any pitch are stored
+// in one piece (the device takes vector accesses at element alignment).
+template <int YT, int C> __device__ __forceinline__ void store_cols_as(const MxArgs& a, int m, int n, float (&v)[C], float factor) {
+  typedef typename Elem<YT>::type E;
+  const bool whole = n + C <= a.N;
+  const int have = min(a.N - n, C);
+#pragma unroll
+  for (int i = 0; i < C; ++i) v[i] *= factor;
+  if (a.resid) {
+    E r[C] = {};
+    const E* rp = reinterpret_cast<const E*>(a.resid) + (int64_t)m * a.ldr + n;
+    if (whole) get(rp, r);
+    else for (int i = 0; i < C; ++i) if (i < have) r[i] = rp[i];
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] += to_f32(r[i]);
+  }
+  E q[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) q[i] = (E)v[i];
+  E* y = reinterpret_cast<E*>(a.y) + (int64_t)m * a.ldy + n;
+  if (whole) put(y, q);
+  else for (int i = 0; i < C; ++i) if (i < have) y[i] = q[i];
+}
+template <int C> __device__ __forceinline__ void store_cols(const MxArgs& a, int m, int n, float (&v)[C], float factor) {
+  if (a.y_type == F32) store_cols_as<F32, C>(a, m, n, v, factor);
+  else if (a.y_type == F16) store_cols_as<F16, C>(a, m, n, v, factor);
+  else store_cols_as<BF16, C>(a, m, n, v, factor);
 }
 
 // A grouped product's slots of expert e, kept within [0, T] whatever the
