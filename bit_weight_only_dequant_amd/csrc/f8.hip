@@ -3,15 +3,17 @@
 // feed-forward block with its activation, and that block's backward pass.
 // The format and the entry points are described in include/qgemm.h.
 //
-// Kernels (times in replayed graphs with the operands in the on-die cache)
+// Kernels (times in replayed graphs of 12 passes with the operands in the
+// on-die cache)
 //   f8_quantize_rows, f8_quantize_tiles, f8_dequantize
 //                   bound by HBM: 8192 x 8192 fp32 in blocks of 128 x 128 67 us
 //                   (5.0 TB/s; a large copy reaches 5.16), bf16 in blocks of 1
 //                   42 us (4.8), turned over 49 us (4.1); read back to fp32 67.
 //   f8_rows         few rows.  W goes from memory straight to registers, x
-//                   through LDS; waves split K.  1 x 6144 x 2048 with fp16 x 5.7
-//                   us, 8 x 2048 x 8192 with bf16 x 8.2, gate and up projection
-//                   of 8192 features of one row 8.5.
+//                   through LDS; waves split K.  1 x 6144 x 2048 with fp16 x 6.3
+//                   us, 8 x 2048 x 8192 with bf16 x and a residual 9.1, gate and
+//                   up projection of 8192 features of one row 9.5 (of 60 passes,
+//                   without the residual: 5.7, 8.2 and 8.7).
 //   f8_tile         more rows.  x and W through a ring of LDS stages by direct
 //                   loads; a stage of 128 k is one block of the scales.  8-bit
 //                   x to bf16: 4096 x 8192 x 8192 256 to 265 us (2.1 PFLOP/s;
@@ -167,12 +169,15 @@ __global__ __launch_bounds__(EW_THREADS) void f8_dequantize_kernel(const uint8_t
 }
 
 // Tiles of 128 x 128: those whose block spans rows, and those that are turned
-// over (8192 x 8192 bf16 47 to 49 us: the stores go out in pieces of 128 bytes).  A lane takes 8 columns of 4 consecutive rows, so that 4 codes of a
-// column are a word.  Largest magnitudes go from lane to lane over a wave's 16
-// rows and through LDS over the waves; turned codes go through LDS in rows of
-// 33 words (a wave's writes touch the 64 banks once), and are stored 32 bytes a
-// lane.  M rows of x; `wide` is the pitch of the turned codes, M rounded up to
-// 16, zeros past M.
+// over (8192 x 8192 bf16 47 to 49 us with blocks of 1, 46 with blocks of 128 x
+// 128: the stores go out in pieces of 128 bytes).  A lane takes 8 columns of 4
+// consecutive rows, so that 4 codes of a column are a word.  Largest magnitudes
+// go from lane to lane over a wave's 16 rows and through LDS over the waves;
+// turned codes go through LDS in rows of 33 words, and are stored 32 bytes a
+// lane.  A wave's writes touch 32 of the 64 banks twice (the columns of lanes c8
+// and c8 + 8 are 64 rows apart, a multiple of 64 words for any pitch), its reads
+// 40 of them up to twice.  M rows of x; `wide` is the pitch of the turned codes,
+// M rounded up to 16, zeros past M.
 template <int T, bool BLOCK, bool TURN>
 __global__ __launch_bounds__(512) void f8_quantize_tiles_kernel(const typename Elem<T>::type* __restrict__ x,
                                                                 int64_t ldx, int M, int K, int wide,
@@ -852,8 +857,9 @@ __global__ __launch_bounds__(WM * WN * KG * 64) __attribute__((amdgpu_waves_per_
   };
 
   // Of a stage's loads the first EARLY are sent for in the last row of blocks, the others along the next stage's first
-  // rows (where all is read ahead: all along the stage).  All in the last row made its waves wait to send: 4096 x 8192 x
-  // 8192 took 306 us there instead of 291, and with 16-bit x 4096 x 2048 x 16384 253 instead of 245.
+  // rows (where all is read ahead: all along the stage).  All in the last row make its waves wait to send: in turn on one
+  // machine, warm from such runs (which take 255 to 265 us from rest), 4096 x 8192 x 8192 303 us instead of 290, gradients
+  // of 4096 x 2048 -> 8192 196 instead of 188; with 16-bit x no difference (4096 x 2048 x 16384 238 to 245 either way).
   constexpr int EARLY = WHOLE ? QALL : C8 ? 4 : 6;
   static_assert(WHOLE || (EARLY <= QALL && (QALL - EARLY - 1) * 2 + 1 < (MI - 1) * NI), "the others are sent for in time");
 #pragma unroll
@@ -1073,15 +1079,15 @@ struct F8Plan { int tile, nw; int64_t workgroups; bool fits; };
 // What the tiles multiply with: 16-bit x, 8-bit x on converted codes, 8-bit x as it is.
 enum { KIND_16 = 0, KIND_EXACT = 1, KIND_FAST = 2 };
 
-// The rule is a model of the time in nanoseconds, fitted to what the kernels took in replayed graphs (48 random
-// shapes of 1..4096 rows, plain and gated, of each kind; on 40 others what it picks is 0.4 to 1.4 % behind the best).  A
-// tile's stage of 128 k takes `alone` when its CU runs one tile and `shared` for each of the CU's tiles when the
-// chip is full; `start` is a tile's first loads and stores, of which the share `more` shows again for every further
-// tile of the CU.  The rows kernel takes 1.3 to 1.9 for a block of 16 x 16 outputs and chunk of 512 k, over the whole chip.
-// For instance 8-bit x to bf16: 383 x 2048 x 4128 on 64 x 64 tiles 15.9 us, on 128 x 128 27; 4096 x
-// 8192 x 8192 on 256 x 256 265, on 128 x 128 403.  The last tile is the first with two groups of waves: 128 x 2048 x
-// 8192 with bf16 x 24.5 us, with one group 32.9; where there are several tiles for a CU they only cost.  Tiles of 64 x
-// 128 and 128 x 128 with two groups were built too and never paid.
+// The rule is a model of the time in nanoseconds, fitted to what the kernels took in replayed graphs (40 random shapes of
+// 1..4096 rows and 8 chosen ones, plain and gated, of each kind; on 40 other random ones what it picks is 0.4 to 1.4 %
+// behind the best).  A tile's stage of 128 k takes `alone` when its CU runs one tile and `shared` for each of the CU's
+// tiles when the chip is full; `start` is a tile's first loads and stores, of which the share `more` shows again for every
+// further tile of the CU.  The rows kernel takes 1.3 to 1.9 for a block of 16 x 16 outputs and chunk of 512 k, over the
+// whole chip.  For instance 8-bit x to bf16: 383 x 2048 x 4128 on 64 x 64 tiles 15.9 us, on 128 x 128 27; 4096 x 8192 x
+// 8192 on 256 x 256 255 to 265, on 128 x 128 403 to 420.  The last tile is the first with two groups of waves: 128 x 2048
+// x 8192 with bf16 x 24.5 us, with one group 33 to 34; where there are several tiles for a CU they only cost.  Tiles of
+// 64 x 128 and 128 x 128 with two groups were built too and never paid.
 struct F8Tile { int rows, cols, groups, waves; double alone, shared, start, more; };   // waves: of a group
 constexpr F8Tile F8_TILES[3][5] = {
     {{64, 64, 1, 4, 475, 364, 3760, 0.39}, {64, 128, 1, 4, 900, 582, 3560, 0.54}, {128, 128, 1, 8, 848, 844, 4800, 1.31},
