@@ -423,7 +423,9 @@ int qmx_plan(int M, int N, int K, int E, int x_type, int out[4]);
  *
  * Conventions: those of the MXFP4 operators above (no workspace, any stream,
  * capturable), with these differences.  K % 16 == 0.  Scales are 4-byte
- * aligned.  The types are numbered on from qg_mx_type_t.
+ * aligned.  The types are numbered on from qg_mx_type_t.  An output overlaps no
+ * input, but for a residual that is y itself: nothing checks it beyond qf8_gated_grad's
+ * d at dh's address, and workgroups read what others have written.
  */
 enum { QG_F8_E4M3 = 4 };
 
