@@ -878,3 +878,22 @@ def test_results_carry_no_graph():
     want, = torch.autograd.grad(torch.nn.functional.silu(p[:, :48]) * p[:, 48:], xd, dh.double())
     gap = (got.double() - want).norm() / want.norm()
     assert gap < 2.0 ** -7, gap   # d and dx rounded once each, by half a step (2^-8) at most
+
+
+@pytest.mark.parametrize("tile", range(6))
+def test_large_products_cancel_across_eights(monkeypatch, tile):
+    # 256 * 256 in one eight, -256 * 256 in another and 6 * 7 in a third, of any lane and block: no eight has to cut (the
+    # 42 lies on its own grid, 2^(2 - 13)), and between them the sum is fp32's
+    monkeypatch.setenv("QF8_TILE", str(tile))
+    M, N, K = 330, 64, 272
+    rng = np.random.default_rng(tile)
+    xv, wv = np.zeros((M, K), np.float32), np.tile(np.array([256, 0] + [4] * 6, np.float32), (N, K // 8))
+    for m in range(M):
+        a, b, c = rng.permutation(K // 8)[:3] * 8
+        xv[m, a], xv[m, b], xv[m, c + 2:c + 8] = 256, -256, 1.75
+    x, w = (torch.from_numpy(v).to(CODE).to(DEV) for v in (xv, wv))
+    one = torch.ones(M, 3, device=DEV)
+    ref, mag = f8ref.f8_gemm_ref(xv.astype(np.float64), wv.astype(np.float64))
+    assert (ref == 42).all()
+    for yt in (F32, BF16):
+        inside(qgm.f8_gemm(x, w, one[:1], x_scales=one, out_dtype=yt), ref, sums(K, mag))
